@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "launch.cuh"
 
 using namespace sba;
@@ -20,6 +21,9 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+}  // namespace
+
+namespace sba {
 // Checks shared by every call that takes a cache.
 int check_cache(const sba_cache* c) {
     if (!c || !c->k || !c->v || !c->seq_lens) return SBA_ERR_INVALID_ARG;
@@ -38,6 +42,9 @@ int check_cache(const sba_cache* c) {
     if (c->kg && !aligned16(c->kg)) return SBA_ERR_INVALID_ARG;
     return SBA_OK;
 }
+}  // namespace sba
+
+namespace {
 
 int check_params(const sba_select_params* p) {
     if (!p) return SBA_ERR_INVALID_ARG;
@@ -288,6 +295,175 @@ int sba_decode_step(const sba_cache* c, const void* q, const void* k_new, const 
                                            out_dtype, lse_out, sel_idx, sel_cnt,
                                            p->scorer == SBA_SCORER_GATE ? gate_bias : nullptr, n_max, C,
                                            static_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Four-bit caches, attention weights, eviction
+// ---------------------------------------------------------------------------
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A four-bit cache seen as a bf16 one: the same checks, and the view that scoring (which reads the
+// descriptors only) takes.
+sba_cache view_of(const sba_cache4& c) {
+    sba_cache v{};
+    v.k = c.kv;
+    v.v = c.kv;
+    v.block_table = c.block_table;
+    v.seq_lens = c.seq_lens;
+    v.B = c.B;
+    v.H_q = c.H_q;
+    v.H_kv = c.H_kv;
+    v.d = c.d;
+    v.b = c.b;
+    v.max_blocks = c.max_blocks;
+    v.num_pages = c.num_pages;
+    v.max_len = c.max_len;
+    v.desc = c.desc;
+    v.status = c.status;
+    return v;
+}
+
+int check_cache4(const sba_cache4* c) {
+    if (!c) return SBA_ERR_INVALID_ARG;
+    const sba_cache v = view_of(*c);
+    const int rc = check_cache(&v);
+    if (rc != SBA_OK) return rc;
+    if (c->B > 65535 || c->H_kv > 65535) return SBA_ERR_UNSUPPORTED;
+    return SBA_OK;
+}
+
+// Arguments of the calls that attend with M query tokens over a selection or (sel_idx NULL) all blocks.
+int check_attend(int H_q, int H_kv, const void* q, int32_t M, const int32_t* sel_idx, const int32_t* sel_cnt,
+                 int32_t n_max, float softmax_scale) {
+    if (!q || !aligned16(q) || M < 1 || M > kMaxQueryTokens || !good_scale(softmax_scale)) return SBA_ERR_INVALID_ARG;
+    if (sel_idx ? (!sel_cnt || n_max < 1) : (sel_cnt != nullptr || n_max != 0)) return SBA_ERR_INVALID_ARG;
+    if ((int64_t)H_kv * (((int64_t)M * (H_q / H_kv) + 7) / 8) > 65535) return SBA_ERR_UNSUPPORTED;
+    return SBA_OK;
+}
+
+int check_weights(const float* lse, const float* acc_in, const float* acc_out) {
+    if (!lse || !acc_in || !acc_out || !aligned4(lse) || !aligned4(acc_in) || !aligned4(acc_out))
+        return SBA_ERR_INVALID_ARG;
+    return SBA_OK;
+}
+
+// Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before).
+int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* p, const sba_cache& dst,
+                const float* acc_dst, const int32_t* new_lens, const int32_t* kept) {
+    if (!acc || !p || !new_lens || !kept) return SBA_ERR_INVALID_ARG;
+    if (p->n_keep < 1 || p->n_sink < 0 || p->n_recent < 0 || (int64_t)p->n_sink + p->n_recent > p->n_keep)
+        return SBA_ERR_INVALID_ARG;
+    if (dst.B != src.B || dst.H_kv != src.H_kv || dst.b != src.b) return SBA_ERR_INVALID_ARG;
+    if ((int64_t)p->n_keep > (int64_t)dst.max_blocks * dst.b) return SBA_ERR_INVALID_ARG;
+    // the lengths are read while the new ones are written, the rows while others are
+    if (new_lens == src.seq_lens || acc_dst == acc || (dst.desc && dst.desc == src.desc && !dst.block_table))
+        return SBA_ERR_INVALID_ARG;
+    if ((dst.k == src.k || dst.v == src.v) && !dst.block_table && !src.block_table) return SBA_ERR_INVALID_ARG;
+    if (src.B > 65535 || src.H_kv > 65535) return SBA_ERR_UNSUPPORTED;
+    return SBA_OK;
+}
+
+}  // namespace
+
+int sba_append_kv4(const sba_cache4* c, const void* k_new, const void* v_new, const int32_t* pos_start, int32_t n_new,
+                   void* stream) {
+    const int rc = check_cache4(c);
+    if (rc != SBA_OK) return rc;
+    if (!k_new || !v_new || !pos_start || n_new < 0) return SBA_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || !aligned16(v_new)) return SBA_ERR_INVALID_ARG;
+    if (n_new == 0) return SBA_OK;
+    return after_launch(launch_append_kv4(*c, k_new, v_new, pos_start, n_new, static_cast<cudaStream_t>(stream)));
+}
+
+int sba_read_kv4(const sba_cache4* c, const int32_t* pos_start, int32_t n, void* k_out, void* v_out, void* stream) {
+    const int rc = check_cache4(c);
+    if (rc != SBA_OK) return rc;
+    if (!k_out || !v_out || !pos_start || n < 0) return SBA_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return SBA_ERR_INVALID_ARG;
+    if (n == 0) return SBA_OK;
+    return after_launch(launch_read_kv4(*c, pos_start, n, k_out, v_out, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sba_score_select_kv4_workspace_size(const sba_cache4* c, const sba_select_params* p) {
+    if (check_cache4(c) != SBA_OK || check_params(p) != SBA_OK) return 0;
+    return score_workspace_bytes(view_of(*c), *p);
+}
+
+int sba_score_select_kv4(const sba_cache4* c, const void* q, int32_t M, const sba_select_params* p, int32_t* sel_idx,
+                         int32_t* sel_cnt, int32_t n_max, void* ws, size_t ws_bytes, void* stream) {
+    const int rc = check_cache4(c);
+    if (rc != SBA_OK) return rc;
+    const sba_cache v = view_of(*c);
+    if (p && p->scorer == SBA_SCORER_GATE) return SBA_ERR_UNSUPPORTED;
+    return sba_score_select_multi(&v, q, M, p, sel_idx, sel_cnt, n_max, ws, ws_bytes, stream);
+}
+
+size_t sba_decode_kv4_workspace_size(const sba_cache4* c, int32_t M, int32_t n_max) {
+    if (check_cache4(c) != SBA_OK || M < 1 || M > kMaxQueryTokens || n_max < 0) return 0;
+    return decode_kv4_workspace_bytes(*c, M, n_max);
+}
+
+int sba_decode_kv4(const sba_cache4* c, const void* q, int32_t M, const int32_t* sel_idx, const int32_t* sel_cnt,
+                   int32_t n_max, float softmax_scale, void* out, int32_t out_dtype, float* lse_out, void* ws,
+                   size_t ws_bytes, void* stream) {
+    int rc = check_cache4(c);
+    if (rc != SBA_OK) return rc;
+    rc = check_attend(c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
+    if (rc != SBA_OK) return rc;
+    if (!out || !aligned16(out) || (out_dtype != SBA_OUT_F32 && out_dtype != SBA_OUT_BF16)) return SBA_ERR_INVALID_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < decode_kv4_workspace_bytes(*c, M, n_max)) return SBA_ERR_WORKSPACE;
+    return after_launch(launch_decode_kv4(*c, q, M, sel_idx, sel_cnt, n_max, softmax_scale, out, out_dtype, lse_out, ws,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+int sba_accumulate_weights(const sba_cache* c, const void* q, int32_t M, const int32_t* sel_idx,
+                           const int32_t* sel_cnt, const float* gate_bias, int32_t n_max, float softmax_scale,
+                           const float* lse, const float* acc_in, float* acc_out, void* stream) {
+    int rc = check_cache(c);
+    if (rc != SBA_OK) return rc;
+    rc = check_attend(c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
+    if (rc != SBA_OK) return rc;
+    if (gate_bias && (!sel_idx || M != 1)) return SBA_ERR_INVALID_ARG;
+    rc = check_weights(lse, acc_in, acc_out);
+    if (rc != SBA_OK) return rc;
+    if (c->B > 65535 || c->H_kv > 65535) return SBA_ERR_UNSUPPORTED;
+    return after_launch(launch_accumulate_weights(*c, q, M, sel_idx, sel_cnt, gate_bias, n_max, softmax_scale, lse,
+                                                  acc_in, acc_out, static_cast<cudaStream_t>(stream)));
+}
+
+int sba_accumulate_weights_kv4(const sba_cache4* c, const void* q, int32_t M, const int32_t* sel_idx,
+                               const int32_t* sel_cnt, int32_t n_max, float softmax_scale, const float* lse,
+                               const float* acc_in, float* acc_out, void* stream) {
+    int rc = check_cache4(c);
+    if (rc != SBA_OK) return rc;
+    rc = check_attend(c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
+    if (rc != SBA_OK) return rc;
+    rc = check_weights(lse, acc_in, acc_out);
+    if (rc != SBA_OK) return rc;
+    return after_launch(launch_accumulate_weights_kv4(*c, q, M, sel_idx, sel_cnt, n_max, softmax_scale, lse, acc_in,
+                                                      acc_out, static_cast<cudaStream_t>(stream)));
+}
+
+int sba_evict(const sba_cache* src, const float* acc, const sba_evict_params* p, const sba_cache* dst, float* acc_dst,
+              int32_t* new_lens, int32_t* kept, void* stream) {
+    int rc = check_cache(src);
+    if (rc == SBA_OK) rc = check_cache(dst);
+    if (rc == SBA_OK) rc = check_evict(*src, acc, p, *dst, acc_dst, new_lens, kept);
+    if (rc != SBA_OK) return rc;
+    return after_launch(launch_evict(*src, acc, *p, *dst, acc_dst, new_lens, kept, static_cast<cudaStream_t>(stream)));
+}
+
+int sba_evict_kv4(const sba_cache4* src, const float* acc, const sba_evict_params* p, const sba_cache4* dst,
+                  float* acc_dst, int32_t* new_lens, int32_t* kept, void* stream) {
+    int rc = check_cache4(src);
+    if (rc == SBA_OK) rc = check_cache4(dst);
+    if (rc == SBA_OK) rc = check_evict(view_of(*src), acc, p, view_of(*dst), acc_dst, new_lens, kept);
+    if (rc != SBA_OK) return rc;
+    return after_launch(
+        launch_evict_kv4(*src, acc, *p, *dst, acc_dst, new_lens, kept, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,324 @@
+// Accumulated attention weights of the cached tokens, per KV head: what an eviction ranks by.
+//
+//   acc_out[t] = acc_in[t] + sum over rows r of exp((q_r . k_t) * scale + bias_r,j(t) - lse_r)
+// over the tokens of the selected blocks (or all blocks), with the rows (token i, head) of the group
+// and the log-sum-exp that the attention of the same step returned: the softmax is not formed again,
+// so one pass over the keys is enough and every token's sum belongs to one thread (no atomics, the
+// same bits on every run).
+//
+// A warp takes 16 tokens at a time: their keys are the rows of f16/bf16 mma.sync tiles (m16n8k16),
+// read straight from global memory into operand registers, with the next tile's keys in flight; the
+// query rows are the columns, 8 at a time, kept in shared memory as operand fragments.  The channels
+// of an MMA step are permuted alike in both so that every lane's key reads are 16 bytes.
+// With few rows the bytes of K bound it (one read of 256 or 72 bytes a token); with many, the MMAs.
+#include <math.h>
+
+#include "common.cuh"
+#include "kv4.cuh"
+#include "launch.cuh"
+
+namespace sba {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTileTokens = 16;
+constexpr int kRowTiles = 16;  // row tiles of 8 staged at a time (128 rows, 32 KB)
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Args {
+    const uint8_t* k;  // bf16 keys or four-bit tiles
+    const int32_t* block_table;
+    const int32_t* seq_lens;
+    int32_t* status;
+    int H_q, H_kv, b, max_blocks, num_pages, M, rows;
+    const __nv_bfloat16* q;
+    const int32_t* sel_idx;
+    const int32_t* sel_cnt;
+    const float* gate_bias;
+    int n_max;
+    float scale_log2;
+    const float* lse;
+    const float* acc_in;
+    float* acc_out;
+};
+
+// The keys of 16 tokens as loaded: lane (tr, i) holds rows tr and tr + 8.
+template <bool kFour>
+struct Keys;
+
+template <>
+struct Keys<false> {  // chunks 4j + i of 8 channels
+    uint4 a[4], c[4];
+    __device__ __forceinline__ void load(const uint8_t* k, int64_t row, int lane) {
+        const uint4* p = reinterpret_cast<const uint4*>(k) + (row + (lane >> 2)) * 16 + (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[j] = ld_once_v4(p + 4 * j);
+            c[j] = ld_once_v4(p + 8 * 16 + 4 * j);
+        }
+    }
+    __device__ __forceinline__ void operand(uint32_t (&f)[8][4]) const {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f[2 * j][0] = a[j].x;
+            f[2 * j][1] = c[j].x;
+            f[2 * j][2] = a[j].y;
+            f[2 * j][3] = c[j].y;
+            f[2 * j + 1][0] = a[j].z;
+            f[2 * j + 1][1] = c[j].z;
+            f[2 * j + 1][2] = a[j].w;
+            f[2 * j + 1][3] = c[j].w;
+        }
+    }
+    // first channel of lane quarter i's pair `half` in MMA step ks
+    static __device__ __forceinline__ int channel(int ks, int i, int half) {
+        return (4 * (ks >> 1) + i) * 8 + 4 * (ks & 1) + 2 * half;
+    }
+};
+
+template <>
+struct Keys<true> {  // channels 32i .. 32i + 31: one 16-byte read a row
+    uint4 a, c;
+    uint32_t sa, sc;
+    __device__ __forceinline__ void load(const uint8_t* k, int64_t row, int lane) {
+        // row counts 32 to a strip; a tile of 16 does not leave its strip
+        const uint8_t* strip = k + (row >> 5) * kStripBytes;
+        const int r = (int)(row & 31) + (lane >> 2), i = lane & 3;
+        a = ld_once_v4(strip + r * 64 + i * 16);
+        c = ld_once_v4(strip + (r + 8) * 64 + i * 16);
+        sa = __ldca(reinterpret_cast<const uint16_t*>(strip + kStripKS + r * 8 + 2 * i));
+        sc = __ldca(reinterpret_cast<const uint16_t*>(strip + kStripKS + (r + 8) * 8 + 2 * i));
+    }
+    __device__ __forceinline__ void operand(uint32_t (&f)[8][4]) const {
+        const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wc[4] = {c.x, c.y, c.z, c.w};
+        const uint32_t fa[2] = {scale_f16x2(sa & 0xff), scale_f16x2(sa >> 8)};
+        const uint32_t fc[2] = {scale_f16x2(sc & 0xff), scale_f16x2(sc >> 8)};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            uint32_t x[4], y[4];
+            codes_to_f16(wa[w], x[0], x[1], x[2], x[3]);
+            codes_to_f16(wc[w], y[0], y[1], y[2], y[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f[2 * w + (e >> 1)][2 * (e & 1)] = mul_f16x2(x[e], fa[w >> 1]);
+                f[2 * w + (e >> 1)][2 * (e & 1) + 1] = mul_f16x2(y[e], fc[w >> 1]);
+            }
+        }
+    }
+    static __device__ __forceinline__ int channel(int ks, int i, int half) { return 32 * i + 4 * ks + 2 * half; }
+};
+
+template <bool kFour>
+__global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a) {
+    __shared__ uint2 qf[kRowTiles][8][32];
+    __shared__ float row_sc[kRowTiles * 8], row_lse[kRowTiles * 8];
+    __shared__ int row_lim[kRowTiles * 8];
+    __shared__ int tile_plain[kRowTiles];  // every row of the tile is real and has a finite lse
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tr = lane >> 2, qi = lane & 3;
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int G = a.H_q / a.H_kv;
+    pdl_wait();
+    pdl_trigger();
+
+    const int len = max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b));
+    const int N = blocks_of(len, a.b);
+    int nb = N;
+    const int32_t* sel = nullptr;
+    if (a.sel_idx) {
+        nb = __ldca(a.sel_cnt + s * a.H_kv + h);
+        if (nb < 0 || nb > a.n_max) {
+            if (tid == 0 && blockIdx.x == 0) report(a.status, SBA_DEV_BAD_SELECTION);
+            nb = nb < 0 ? 0 : a.n_max;
+        }
+        sel = a.sel_idx + ((int64_t)s * a.H_kv + h) * a.n_max;
+    }
+    const int tpb = a.b / kTileTokens;
+    const int64_t T = (int64_t)nb * tpb;
+    const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
+    if (t0 >= t1) return;
+    const int mine = t0 + warp < t1 ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
+
+    // lane x resolves this warp's tile 32 * batch + x: cache row (page, head, row) of its first token
+    int64_t row = -1;
+    int tok = 0, pos = 0;
+    auto resolve = [&](int x) {
+        row = -1;
+        if (x >= mine) return;
+        const int g = t0 + warp + kWarps * x;
+        pos = g / tpb;
+        const int j = sel ? __ldca(sel + pos) : pos;
+        // ascending: a block listed twice would be written by two warps
+        if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
+            report(a.status, SBA_DEV_BAD_SELECTION);
+            return;
+        }
+        const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
+        tok = j * a.b + (g % tpb) * kTileTokens;
+        if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % tpb) * kTileTokens;
+    };
+
+    for (int r0 = 0; r0 < a.rows; r0 += kRowTiles * 8) {
+        const int n_rows = min(kRowTiles * 8, a.rows - r0), n_tiles = (n_rows + 7) / 8;
+        // ---- the rows' operand fragments, scales, lse and limits ----
+        if (r0) __syncthreads();
+        for (int t = warp; t < n_tiles; t += kWarps) {
+            const int r = r0 + t * 8 + tr;
+            const bool real = r < a.rows;
+            const int64_t qrow = real ? ((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G : 0;
+            const __nv_bfloat16* p = a.q + qrow * kHeadDim;
+            uint32_t w[8][2];
+            float mx = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t v =
+                        real ? __ldca(reinterpret_cast<const uint32_t*>(p + Keys<kFour>::channel(ks, qi, half))) : 0u;
+                    w[ks][half] = v;
+                    mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(v)), fabsf(bf16_hi(v))));
+                }
+            float up = 1.f;
+            if (kFour) {  // f16 operands: the row scaled by a power of two to a maximum in [1, 2)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int e = row_exponent(mx);
+                const float down = pow2(-e);
+                up = pow2(e);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        w[ks][half] = pack_f16(bf16_lo(w[ks][half]) * down, bf16_hi(w[ks][half]) * down);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) qf[t][ks][lane] = make_uint2(w[ks][0], w[ks][1]);
+            const float lse = real ? __ldca(a.lse + qrow) : -INFINITY;
+            const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
+            if (qi == 0) {
+                row_sc[t * 8 + tr] = a.scale_log2 * up;
+                row_lse[t * 8 + tr] = counts ? lse * kLog2e : 0.f;
+                row_lim[t * 8 + tr] = counts ? len - a.M + r / G + 1 : 0;
+            }
+            const int all = __all_sync(0xffffffffu, counts);
+            if (lane == 0) tile_plain[t] = all;
+        }
+        __syncthreads();
+
+        const float* acc_from = r0 ? a.acc_out : a.acc_in;
+        const int first_hidden = len - a.M + 1;
+        Keys<kFour> next;
+        auto fetch = [&](int x) {
+            if ((x & 31) == 0) resolve(x + lane);
+            const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
+            if (from >= 0) next.load(a.k, from, lane);
+        };
+        int64_t cur_row = -1;
+        int cur_tok = 0, cur_pos = 0;
+        if (mine > 0) fetch(0);
+        for (int x = 0; x < mine; ++x) {
+            cur_row = __shfl_sync(0xffffffffu, row, x & 31);
+            cur_tok = __shfl_sync(0xffffffffu, tok, x & 31);
+            cur_pos = __shfl_sync(0xffffffffu, pos, x & 31);
+            uint32_t kf[8][4];
+            next.operand(kf);
+            if (x + 1 < mine) fetch(x + 1);
+            if (cur_row < 0) continue;
+            float w0 = 0.f, w1 = 0.f;
+            const bool all_seen = cur_tok + kTileTokens <= first_hidden;
+            for (int t = 0; t < n_tiles; ++t) {
+                float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < 8; ks += 2) {
+                    const uint2 b0 = qf[t][ks][lane], b1 = qf[t][ks + 1][lane];
+                    if (kFour) {
+                        mma_f16_16816(e, kf[ks], b0.x, b0.y);
+                        mma_f16_16816(o, kf[ks + 1], b1.x, b1.y);
+                    } else {
+                        mma_bf16_16816(e, kf[ks], b0.x, b0.y);
+                        mma_bf16_16816(o, kf[ks + 1], b1.x, b1.y);
+                    }
+                }
+                const int r = t * 8 + 2 * qi;
+                const float2 sc = *reinterpret_cast<const float2*>(&row_sc[r]);
+                float2 off = *reinterpret_cast<const float2*>(&row_lse[r]);
+                if (a.gate_bias) {
+                    const int64_t at = ((int64_t)s * a.H_q + h * G + r0 + r) * a.n_max + cur_pos;
+                    if (r0 + r < a.rows) off.x -= __ldca(a.gate_bias + at) * kLog2e;
+                    if (r0 + r + 1 < a.rows) off.y -= __ldca(a.gate_bias + at + a.n_max) * kLog2e;
+                }
+                float p0 = ex2(fmaf(e[0] + o[0], sc.x, -off.x)), p1 = ex2(fmaf(e[1] + o[1], sc.y, -off.y));
+                float p2 = ex2(fmaf(e[2] + o[2], sc.x, -off.x)), p3 = ex2(fmaf(e[3] + o[3], sc.y, -off.y));
+                if (!all_seen || !tile_plain[t]) {
+                    const int2 lim = *reinterpret_cast<const int2*>(&row_lim[r]);
+                    if (cur_tok + tr >= lim.x) p0 = 0.f;
+                    if (cur_tok + tr >= lim.y) p1 = 0.f;
+                    if (cur_tok + tr + 8 >= lim.x) p2 = 0.f;
+                    if (cur_tok + tr + 8 >= lim.y) p3 = 0.f;
+                }
+                w0 += p0 + p1;
+                w1 += p2 + p3;
+            }
+            w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+            w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+            w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+            w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+            if (qi < 2) {  // lane 0 of a quad writes token tr, lane 1 token tr + 8
+                const int t = tr + 8 * qi;
+                if (cur_tok + t < len) a.acc_out[cur_row + t] = acc_from[cur_row + t] + (qi ? w1 : w0);
+            }
+        }
+    }
+}
+
+template <bool kFour, class Cache>
+int launch_weights(const Cache& c, const void* keys, const void* q, int M, const int32_t* sel_idx,
+                   const int32_t* sel_cnt, const float* gate_bias, int n_max, float scale, const float* lse,
+                   const float* acc_in, float* acc_out, cudaStream_t stream) {
+    Args a{};
+    a.k = static_cast<const uint8_t*>(keys);
+    a.block_table = c.block_table;
+    a.seq_lens = c.seq_lens;
+    a.status = c.status;
+    a.H_q = c.H_q;
+    a.H_kv = c.H_kv;
+    a.b = c.b;
+    a.max_blocks = c.max_blocks;
+    a.num_pages = c.num_pages;
+    a.M = M;
+    a.rows = M * (c.H_q / c.H_kv);
+    a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+    a.sel_idx = sel_idx;
+    a.sel_cnt = sel_cnt;
+    a.gate_bias = gate_bias;
+    a.n_max = n_max;
+    a.scale_log2 = scale * kLog2e;
+    a.lse = lse;
+    a.acc_in = acc_in;
+    a.acc_out = acc_out;
+    // one tile a warp at least; up to eight CTAs per SM's worth of them, so ragged lengths even out
+    const int64_t tiles = (int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kTileTokens);
+    const int64_t most = (tiles + kWarps - 1) / kWarps, want = 8 * 148 / ((int64_t)c.B * c.H_kv);
+    const int64_t x = want < 1 ? 1 : want;
+    dim3 grid((unsigned)(x < most ? x : most < 1 ? 1 : most), c.H_kv, c.B);
+    return launch(accumulate_weights_kernel<kFour>, grid, dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace
+
+int launch_accumulate_weights(const sba_cache& c, const void* q, int M, const int32_t* sel_idx, const int32_t* sel_cnt,
+                              const float* gate_bias, int n_max, float scale, const float* lse, const float* acc_in,
+                              float* acc_out, cudaStream_t stream) {
+    return launch_weights<false>(c, c.k, q, M, sel_idx, sel_cnt, gate_bias, n_max, scale, lse, acc_in, acc_out, stream);
+}
+
+int launch_accumulate_weights_kv4(const sba_cache4& c, const void* q, int M, const int32_t* sel_idx,
+                                  const int32_t* sel_cnt, int n_max, float scale, const float* lse,
+                                  const float* acc_in, float* acc_out, cudaStream_t stream) {
+    return launch_weights<true>(c, c.kv, q, M, sel_idx, sel_cnt, nullptr, n_max, scale, lse, acc_in, acc_out, stream);
+}
+
+}  // namespace sba

@@ -86,8 +86,36 @@ class sba_select_params(ctypes.Structure):
     ]
 
 
+class sba_cache4(ctypes.Structure):
+    _fields_ = [
+        ("kv", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("B", ctypes.c_int32),
+        ("H_q", ctypes.c_int32),
+        ("H_kv", ctypes.c_int32),
+        ("d", ctypes.c_int32),
+        ("b", ctypes.c_int32),
+        ("max_blocks", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_len", ctypes.c_int32),
+        ("desc", ctypes.c_void_p),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class sba_evict_params(ctypes.Structure):
+    _fields_ = [("n_keep", ctypes.c_int32), ("n_sink", ctypes.c_int32), ("n_recent", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_C = ctypes.POINTER(sba_cache)
+_C4 = ctypes.POINTER(sba_cache4)
+_SEL = ctypes.POINTER(sba_select_params)
+_EV = ctypes.POINTER(sba_evict_params)
+_F = ctypes.c_float
+_Z = ctypes.c_size_t
 _SIGS = {
     "sba_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "sba_last_cuda_error": ([], ctypes.c_char_p),
@@ -118,6 +146,16 @@ _SIGS = {
     "sba_decode_step_cluster": ([ctypes.POINTER(sba_cache), ctypes.POINTER(sba_select_params)], _I),
     "sba_decode_step": ([ctypes.POINTER(sba_cache), _P, _P, _P, _P, _I, _P, ctypes.POINTER(sba_select_params),
                          ctypes.c_float, _P, _I, _P, _P, _P, _P, _I, _P], ctypes.c_int),
+    "sba_append_kv4": ([_C4, _P, _P, _P, _I, _P], ctypes.c_int),
+    "sba_read_kv4": ([_C4, _P, _I, _P, _P, _P], ctypes.c_int),
+    "sba_score_select_kv4_workspace_size": ([_C4, _SEL], _Z),
+    "sba_score_select_kv4": ([_C4, _P, _I, _SEL, _P, _P, _I, _P, _Z, _P], ctypes.c_int),
+    "sba_decode_kv4_workspace_size": ([_C4, _I, _I], _Z),
+    "sba_decode_kv4": ([_C4, _P, _I, _P, _P, _I, _F, _P, _I, _P, _P, _Z, _P], ctypes.c_int),
+    "sba_accumulate_weights": ([_C, _P, _I, _P, _P, _P, _I, _F, _P, _P, _P, _P], ctypes.c_int),
+    "sba_accumulate_weights_kv4": ([_C4, _P, _I, _P, _P, _I, _F, _P, _P, _P, _P], ctypes.c_int),
+    "sba_evict": ([_C, _P, _EV, _C, _P, _P, _P, _P], ctypes.c_int),
+    "sba_evict_kv4": ([_C4, _P, _EV, _C4, _P, _P, _P, _P], ctypes.c_int),
 }
 
 _lib = None
@@ -371,6 +409,235 @@ def sba_decode_step(c: Cache, q: torch.Tensor, p: sba_select_params, softmax_sca
                                   n_new, _ptr(gate_A), ctypes.byref(p), float(softmax_scale), _ptr(out), dt,
                                   _ptr(lse_out), _ptr(sel_idx), _ptr(sel_cnt), _ptr(gate_bias), n_max,
                                   _stream(stream)), "sba_decode_step")
+
+
+# ---------------------------------------------------------------------------
+# Four-bit caches, accumulated attention weights, eviction
+# ---------------------------------------------------------------------------
+
+STRIP_TOKENS = 32
+STRIP_BYTES = 4608
+
+
+@dataclass
+class Cache4:
+    """Device tensors of one layer's four-bit KV cache and its Quest descriptors (sba_cache4)."""
+
+    kv: torch.Tensor                       # uint8 [num_pages][H_kv][b/32][4608]
+    seq_lens: torch.Tensor                 # int32 [B]
+    H_q: int
+    max_blocks: int
+    max_len: int
+    block_table: Optional[torch.Tensor] = None   # int32 [B][max_blocks]
+    desc: Optional[torch.Tensor] = None          # bf16 [num_pages][H_kv][2][d]
+    status: Optional[torch.Tensor] = None        # int32 [1]
+
+    @property
+    def num_pages(self) -> int:
+        return int(self.kv.shape[0])
+
+    @property
+    def H_kv(self) -> int:
+        return int(self.kv.shape[1])
+
+    @property
+    def b(self) -> int:
+        return int(self.kv.shape[2]) * STRIP_TOKENS
+
+    @property
+    def d(self) -> int:
+        return 128
+
+    @property
+    def B(self) -> int:
+        return int(self.seq_lens.shape[0])
+
+    def struct(self) -> sba_cache4:
+        # rebuilt only when a tensor of the cache is replaced (in-place updates keep the pointers)
+        key = (id(self.kv), id(self.block_table), id(self.seq_lens), id(self.desc), id(self.status), self.H_q,
+               self.max_blocks, self.max_len)
+        cached = self.__dict__.get("_struct")
+        if cached is None or cached[0] != key:
+            dev = self.kv.device
+            if self.kv.dim() != 4 or self.kv.shape[3] != STRIP_BYTES:
+                raise ValueError(f"kv must be uint8 [num_pages][H_kv][b/32][{STRIP_BYTES}]")
+            _tensor(self.seq_lens, torch.int32, dev, self.B, "seq_lens")
+            _tensor(self.block_table, torch.int32, dev, self.B * self.max_blocks, "block_table")
+            _tensor(self.desc, torch.bfloat16, dev, self.num_pages * self.H_kv * 2 * self.d, "desc")
+            _tensor(self.status, torch.int32, dev, 1, "status")
+            st = sba_cache4(_tensor(self.kv, torch.uint8, dev, 0, "kv"), _ptr(self.block_table), _ptr(self.seq_lens),
+                            self.B, self.H_q, self.H_kv, self.d, self.b, self.max_blocks, self.num_pages, self.max_len,
+                            _ptr(self.desc), _ptr(self.status))
+            # the tensors themselves stay in the key's reach, so that an id is not met again on another one
+            cached = (key, st, ctypes.byref(st), (self.kv, self.block_table, self.seq_lens, self.desc, self.status))
+            self.__dict__["_struct"] = cached
+        return cached[1]
+
+
+def _tensor(t: Optional[torch.Tensor], dtype: torch.dtype, device: torch.device, least: int, name: str):
+    """Pointer of a contiguous tensor of `dtype` on `device` with at least `least` elements (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device} with at least {least} elements "
+                         f"(got {t.dtype} on {t.device}, {t.numel()} elements"
+                         f"{'' if t.is_contiguous() else ', not contiguous'})")
+    return t.data_ptr()
+
+
+def _current(device: torch.device, stream):
+    """The stream to launch on; kernels run on the current device, so the tensors have to be there."""
+    if device.type != "cuda":
+        raise ValueError("libsba takes device tensors only")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return _stream(stream)
+
+
+def _device_of(c) -> torch.device:
+    return c.kv.device if isinstance(c, Cache4) else c.k.device
+
+
+def _rows_of(c, q: torch.Tensor):
+    """Pointer of q ([B][H_q][d], or [B][M][H_q][d]) and M."""
+    M = int(q.shape[1]) if q.dim() == 4 else 1
+    want = (c.B, M, c.H_q, c.d) if q.dim() == 4 else (c.B, c.H_q, c.d)
+    if tuple(q.shape) != want:
+        raise ValueError(f"q must be [B][H_q][d] or [B][M][H_q][d] (got {tuple(q.shape)} for {want})")
+    return _tensor(q, torch.bfloat16, _device_of(c), 0, "q"), M
+
+
+def _selection(c, sel_idx, sel_cnt):
+    """Pointers of a selection and its row length (None, None, 0: every block)."""
+    if sel_idx is None:
+        if sel_cnt is not None:
+            raise ValueError("sel_cnt without sel_idx")
+        return None, None, 0
+    if sel_cnt is None or sel_idx.dim() != 3 or tuple(sel_idx.shape[:2]) != (c.B, c.H_kv):
+        raise ValueError("sel_idx must be int32 [B][H_kv][n_max], with sel_cnt [B][H_kv]")
+    dev = _device_of(c)
+    return (_tensor(sel_idx, torch.int32, dev, 0, "sel_idx"), _tensor(sel_cnt, torch.int32, dev, c.B * c.H_kv, "sel_cnt"),
+            int(sel_idx.shape[2]))
+
+
+def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_params:
+    return sba_evict_params(n_keep, n_sink, n_recent)
+
+
+def sba_append_kv4(c: Cache4, k_new: torch.Tensor, v_new: torch.Tensor, pos_start: torch.Tensor, stream=None):
+    """k_new, v_new: bf16 [B][n_new][H_kv][d] to positions pos_start[s] .. of a four-bit cache."""
+    st, dev = c.struct(), c.kv.device
+    n_new = int(k_new.shape[1])
+    rows = c.B * n_new * c.H_kv * c.d
+    _check(load().sba_append_kv4(ctypes.byref(st), _tensor(k_new, torch.bfloat16, dev, rows, "k_new"),
+                                 _tensor(v_new, torch.bfloat16, dev, rows, "v_new"),
+                                 _tensor(pos_start, torch.int32, dev, c.B, "pos_start"), n_new,
+                                 _current(dev, stream)), "sba_append_kv4")
+
+
+def sba_read_kv4(c: Cache4, pos_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
+    """Positions pos_start[s] .. as bf16 rows k_out, v_out [B][n][H_kv][d]."""
+    st, dev = c.struct(), c.kv.device
+    n = int(k_out.shape[1])
+    rows = c.B * n * c.H_kv * c.d
+    _check(load().sba_read_kv4(ctypes.byref(st), _tensor(pos_start, torch.int32, dev, c.B, "pos_start"), n,
+                               _tensor(k_out, torch.bfloat16, dev, rows, "k_out"),
+                               _tensor(v_out, torch.bfloat16, dev, rows, "v_out"), _current(dev, stream)),
+           "sba_read_kv4")
+
+
+def sba_score_select_kv4_workspace_size(c: Cache4, p: sba_select_params) -> int:
+    return int(load().sba_score_select_kv4_workspace_size(ctypes.byref(c.struct()), ctypes.byref(p)))
+
+
+def sba_score_select_kv4(c: Cache4, q: torch.Tensor, p: sba_select_params, sel_idx: torch.Tensor,
+                         sel_cnt: torch.Tensor, ws: torch.Tensor, stream=None):
+    """q: bf16 [B][H_q][d] or [B][M][H_q][d]; one Quest selection per (sequence, group)."""
+    st, (qp, M) = c.struct(), _rows_of(c, q)
+    si, sc, n_max = _selection(c, sel_idx, sel_cnt)
+    _check(load().sba_score_select_kv4(ctypes.byref(st), qp, M, ctypes.byref(p), si, sc, n_max,
+                                       _tensor(ws, torch.uint8, c.kv.device, 0, "ws"), ws.numel(),
+                                       _current(c.kv.device, stream)), "sba_score_select_kv4")
+
+
+def sba_decode_kv4_workspace_size(c: Cache4, M: int = 1, n_max: int = 0) -> int:
+    return int(load().sba_decode_kv4_workspace_size(ctypes.byref(c.struct()), M, n_max))
+
+
+def sba_decode_kv4(c: Cache4, q: torch.Tensor, softmax_scale: float, out: torch.Tensor, ws: torch.Tensor,
+                   lse_out: Optional[torch.Tensor] = None, sel_idx: Optional[torch.Tensor] = None,
+                   sel_cnt: Optional[torch.Tensor] = None, stream=None):
+    """Attention over the selected blocks (or all) of a four-bit cache.  q, out: [B][H_q][d] or
+    [B][M][H_q][d]; lse_out fp32 [B][M][H_q]; ws: uint8, zeroed once, of
+    sba_decode_kv4_workspace_size(c, M, n_max) bytes."""
+    st, dev = c.struct(), c.kv.device
+    qp, M = _rows_of(c, q)
+    si, sc, n_max = _selection(c, sel_idx, sel_cnt)
+    if out.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out must be fp32 or bf16")
+    rows = c.B * M * c.H_q
+    _check(load().sba_decode_kv4(ctypes.byref(st), qp, M, si, sc, n_max, softmax_scale,
+                                 _tensor(out, out.dtype, dev, rows * c.d, "out"),
+                                 SBA_OUT_BF16 if out.dtype == torch.bfloat16 else SBA_OUT_F32,
+                                 _tensor(lse_out, torch.float32, dev, rows, "lse_out"),
+                                 _tensor(ws, torch.uint8, dev, 0, "ws"), ws.numel(), _current(dev, stream)),
+           "sba_decode_kv4")
+
+
+def _weights_args(c, q, lse, acc_in, acc_out, sel_idx, sel_cnt):
+    dev = _device_of(c)
+    qp, M = _rows_of(c, q)
+    si, sc, n_max = _selection(c, sel_idx, sel_cnt)
+    cells = c.num_pages * c.H_kv * c.b
+    return (qp, M, si, sc, n_max, _tensor(lse, torch.float32, dev, c.B * M * c.H_q, "lse"),
+            _tensor(acc_in, torch.float32, dev, cells, "acc_in"), _tensor(acc_out, torch.float32, dev, cells, "acc_out"))
+
+
+def sba_accumulate_weights(c: Cache, q: torch.Tensor, lse: torch.Tensor, softmax_scale: float, acc_in: torch.Tensor,
+                           acc_out: torch.Tensor, sel_idx: Optional[torch.Tensor] = None,
+                           sel_cnt: Optional[torch.Tensor] = None, gate_bias: Optional[torch.Tensor] = None,
+                           stream=None):
+    """acc_out[t] = acc_in[t] + the attention weight token t received from q's rows (fp32
+    [num_pages][H_kv][b]; acc_out may be acc_in); lse as the step's attention returned it."""
+    st = c.struct()
+    qp, M, si, sc, n_max, lp, ai, ao = _weights_args(c, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
+    gb = _tensor(gate_bias, torch.float32, c.k.device, c.B * c.H_q * n_max, "gate_bias")
+    _check(load().sba_accumulate_weights(ctypes.byref(st), qp, M, si, sc, gb, n_max, softmax_scale, lp, ai, ao,
+                                         _current(c.k.device, stream)), "sba_accumulate_weights")
+
+
+def sba_accumulate_weights_kv4(c: Cache4, q: torch.Tensor, lse: torch.Tensor, softmax_scale: float,
+                               acc_in: torch.Tensor, acc_out: torch.Tensor, sel_idx: Optional[torch.Tensor] = None,
+                               sel_cnt: Optional[torch.Tensor] = None, stream=None):
+    """sba_accumulate_weights on a four-bit cache."""
+    st = c.struct()
+    qp, M, si, sc, n_max, lp, ai, ao = _weights_args(c, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
+    _check(load().sba_accumulate_weights_kv4(ctypes.byref(st), qp, M, si, sc, n_max, softmax_scale, lp, ai, ao,
+                                             _current(c.kv.device, stream)), "sba_accumulate_weights_kv4")
+
+
+def _evict(call, name, src, acc, p, dst, new_lens, kept, acc_dst, stream):
+    ss, ds, dev = src.struct(), dst.struct(), _device_of(src)
+    if _device_of(dst) != dev:
+        raise ValueError("source and destination caches are on different devices")
+    _check(call(ctypes.byref(ss), _tensor(acc, torch.float32, dev, src.num_pages * src.H_kv * src.b, "acc"),
+                ctypes.byref(p), ctypes.byref(ds),
+                _tensor(acc_dst, torch.float32, dev, dst.num_pages * dst.H_kv * dst.b, "acc_dst"),
+                _tensor(new_lens, torch.int32, dev, src.B, "new_lens"),
+                _tensor(kept, torch.int32, dev, src.B * src.H_kv * p.n_keep, "kept"), _current(dev, stream)), name)
+
+
+def sba_evict(src: Cache, acc: torch.Tensor, p: sba_evict_params, dst: Cache, new_lens: torch.Tensor,
+              kept: torch.Tensor, acc_dst: Optional[torch.Tensor] = None, stream=None):
+    """Keep p.n_keep tokens per (sequence, KV head) of src and move them, in order, to dst's pages.
+    new_lens int32 [B] and kept int32 [B][H_kv][n_keep] are written."""
+    _evict(load().sba_evict, "sba_evict", src, acc, p, dst, new_lens, kept, acc_dst, stream)
+
+
+def sba_evict_kv4(src: Cache4, acc: torch.Tensor, p: sba_evict_params, dst: Cache4, new_lens: torch.Tensor,
+                  kept: torch.Tensor, acc_dst: Optional[torch.Tensor] = None, stream=None):
+    """sba_evict on four-bit caches."""
+    _evict(load().sba_evict_kv4, "sba_evict_kv4", src, acc, p, dst, new_lens, kept, acc_dst, stream)
 
 
 # ---------------------------------------------------------------------------

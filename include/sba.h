@@ -162,6 +162,36 @@ typedef struct sba_select_params {
     int32_t gate_act; /* SBA_GATE_SOFTMAX, _SIGMOID or _RAW */
 } sba_select_params;
 
+/* The four-bit form of the KV cache of ONE attention layer: 144 bytes per token and KV head instead
+ * of 512.  Fields as sba_cache, but for:
+ *
+ * kv            device bytes [num_pages][H_kv][b/32][4608], 16-byte aligned: 32 tokens of one head
+ *               make a strip of key codes [32][64], value codes [32][64], key scales [32][8], value
+ *               scales [32][8].  Channel c is the low (c even) or high (c odd) nibble of code byte
+ *               c/2: sign, then one of 0, .5, 1, 1.5, 2, 3, 4, 6 (e2m1).  Scale byte g belongs to
+ *               channels 16g .. 16g+15: five exponent bits (bias 15) and three mantissa bits, the top
+ *               byte of a positive f16 below its sign (byte << 7 are its bits).  A value is
+ *               code * scale; it is exact in f16 and in bf16.
+ * desc          Quest descriptors of the keys AS HELD, bf16 [num_pages][H_kv][2][d], or NULL.
+ *
+ * Only the Quest scorer has a four-bit form (a gate key is formed from bf16 keys). */
+typedef struct sba_cache4 {
+    void *kv;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int32_t B, H_q, H_kv, d, b, max_blocks, num_pages, max_len;
+    void *desc;
+    int32_t *status;
+} sba_cache4;
+
+/* What an eviction keeps of every (sequence, KV head): the first n_sink and the last n_recent tokens
+ * and the heaviest of the rest, n_keep in all (n_sink + n_recent <= n_keep). */
+typedef struct sba_evict_params {
+    int32_t n_keep;
+    int32_t n_sink;
+    int32_t n_recent;
+} sba_evict_params;
+
 /* Message for a status code (static string, never NULL). */
 const char *sba_status_string(int status);
 
@@ -396,6 +426,94 @@ int sba_decode_step(const sba_cache *c, const void *q, const void *k_new, const 
                     const sba_select_params *p, float softmax_scale, void *out, int32_t out_dtype,
                     float *lse_out, int32_t *sel_idx, int32_t *sel_cnt, float *gate_bias, int32_t n_max,
                     void *stream);
+
+/* ------------------------------------------------------------------------
+ * A smaller cache: four-bit rows, and eviction by accumulated attention weight
+ * ------------------------------------------------------------------------ */
+
+/* Write n_new tokens per sequence into four-bit pages, as sba_append_kv does into bf16 ones, and
+ * recompute the Quest descriptors (c->desc, when non-NULL) of the blocks they touch from all of each
+ * block's valid keys as held, as sba_update_descriptors does: one launch.
+ * The scale of 16 channels is the smallest e5m3 value that is at least max|x| / 6 (at most 10240:
+ * larger magnitudes than 61440 are held as 61440); a code is x / scale rounded to the nearest, ties to
+ * the even code.  A group that holds a NaN or an infinity reads back as NaN in all 16 channels.  The
+ * sign of a zero is not kept.
+ * k_new, v_new  device bf16 [B][n_new][H_kv][d], pos_start device int32 [B].
+ * The caller advances seq_lens to include the tokens BEFORE the call; rows at or past len_s are
+ * written, but count in no descriptor.  A sequence whose positions do not lie in [0, max_blocks*b)
+ * reports SBA_DEV_BAD_POSITION and is left alone.  A page belongs to one sequence of a call. */
+int sba_append_kv4(const sba_cache4 *c, const void *k_new, const void *v_new, const int32_t *pos_start,
+                   int32_t n_new, void *stream);
+
+/* Read positions [pos_start[s], pos_start[s] + n) of every sequence back as bf16 rows
+ * k_out, v_out [B][n][H_kv][d] (device): exactly the values the attention uses.  Rows at or past
+ * len_s, or on a bad page, are left as they were.  Positions outside [0, max_blocks*b) report
+ * SBA_DEV_BAD_POSITION. */
+int sba_read_kv4(const sba_cache4 *c, const int32_t *pos_start, int32_t n, void *k_out, void *v_out, void *stream);
+
+/* sba_score_select_multi on a four-bit cache (M = 1 for a decode step): reads the descriptors only.
+ * Quest scorer only (SBA_ERR_UNSUPPORTED for the gate).  ws as for sba_score_select, of at least
+ * sba_score_select_kv4_workspace_size() bytes. */
+size_t sba_score_select_kv4_workspace_size(const sba_cache4 *c, const sba_select_params *p);
+int sba_score_select_kv4(const sba_cache4 *c, const void *q, int32_t M, const sba_select_params *p,
+                         int32_t *sel_idx, int32_t *sel_cnt, int32_t n_max, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/* Attention of M query tokens per sequence over a four-bit cache, split over the sequence and merged
+ * in ONE launch.  q device bf16 [B][M][H_q][d]; token i sits at position len_s - M + i and sees
+ * t <= len_s - M + i, as in sba_sparse_decode_multi.
+ * sel_idx, sel_cnt  the selected blocks as sba_score_select writes them (device int32
+ *                   [B][H_kv][n_max], [B][H_kv]); or both NULL with n_max = 0: every block.  A block
+ *                   listed twice is attended to twice.
+ * out       device [B][M][H_q][d] in out_dtype (SBA_OUT_F32 or SBA_OUT_BF16), 16-byte aligned;
+ *           0 for a row that sees no token.
+ * lse_out   device fp32 [B][M][H_q] or NULL: log sum exp of the row's logits, -inf if it sees none.
+ * ws        device workspace of at least sba_decode_kv4_workspace_size() bytes (same cache shape, M and
+ *           n_max), 16-byte aligned, ZERO-FILLED before its first use; every completed call leaves its
+ *           counters at zero again.  Calls that share a workspace must not run concurrently, and one
+ *           workspace serves one (cache shape, M, n_max): other shapes lay it out differently, so zero
+ *           it again in between. */
+size_t sba_decode_kv4_workspace_size(const sba_cache4 *c, int32_t M, int32_t n_max);
+int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t *sel_idx, const int32_t *sel_cnt,
+                   int32_t n_max, float softmax_scale, void *out, int32_t out_dtype, float *lse_out, void *ws,
+                   size_t ws_bytes, void *stream);
+
+/* Accumulate the attention weight that cached tokens received in a step, per KV head:
+ *   acc_out[t] = acc_in[t] + sum over the group's heads and the M query tokens that see t of
+ *                exp((q . k_t) * softmax_scale [+ gate_bias of t's block] - lse)
+ * for every valid token t of the selected blocks (sel_idx and sel_cnt NULL, n_max = 0: of all blocks).
+ * acc_out of other tokens is left as it was.
+ * lse           device fp32 [B][M][H_q], as the attention of the same step returned it; a row whose lse
+ *               is -inf adds nothing.
+ * gate_bias     as sba_sparse_decode (fp32 [B][H_q][n_max]), or NULL; needs a selection and M = 1.
+ * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); may be the same.
+ * A selection lists every block once, ascending (SBA_DEV_BAD_SELECTION otherwise, and the block is
+ * skipped).  No atomics: the same inputs give the same bits. */
+int sba_accumulate_weights(const sba_cache *c, const void *q, int32_t M, const int32_t *sel_idx,
+                           const int32_t *sel_cnt, const float *gate_bias, int32_t n_max, float softmax_scale,
+                           const float *lse, const float *acc_in, float *acc_out, void *stream);
+int sba_accumulate_weights_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t *sel_idx,
+                               const int32_t *sel_cnt, int32_t n_max, float softmax_scale, const float *lse,
+                               const float *acc_in, float *acc_out, void *stream);
+
+/* Evict: every (sequence, KV head) of `src` keeps min(len_s, n_keep) tokens -- the first n_sink, the
+ * last n_recent and the heaviest of the others by `acc` (fp32 [num_pages][H_kv][b] of src; weight
+ * descending, then position ascending; -0 == +0; a NaN ranks below every number) -- and their K/V rows
+ * are copied, in order, to positions 0, 1, ... of `dst`.  The keys must carry their position
+ * themselves (rotary embeddings applied before caching), since a token's slot changes.
+ * dst        a cache of the same B, H_kv and b whose pages are not pages of src (the same pool with
+ *            another block table, or another pool); n_keep <= dst->max_blocks * b.  dst->seq_lens is not
+ *            read (new_lens is a good value for it).  dst->desc, when non-NULL, receives the Quest
+ *            descriptors of the blocks written; gate keys are not refreshed (call
+ *            sba_update_descriptors for them).  Rows of dst past the kept ones are left as they were.
+ * acc_dst    device fp32 [dst->num_pages][H_kv][b] or NULL: the kept tokens' weights; not acc itself.
+ * new_lens   device int32 [B]: min(len_s, n_keep); not src->seq_lens itself.
+ * kept       device int32 [B][H_kv][n_keep]: the kept positions in src, ascending; entries past the
+ *            new length are left as they were. */
+int sba_evict(const sba_cache *src, const float *acc, const sba_evict_params *p, const sba_cache *dst,
+              float *acc_dst, int32_t *new_lens, int32_t *kept, void *stream);
+int sba_evict_kv4(const sba_cache4 *src, const float *acc, const sba_evict_params *p, const sba_cache4 *dst,
+                  float *acc_dst, int32_t *new_lens, int32_t *kept, void *stream);
 
 #ifdef __cplusplus
 }
