@@ -353,7 +353,7 @@ int check_weights(const float* lse, const float* acc_in, const float* acc_out) {
 // Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before).
 int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* p, const sba_cache& dst,
                 const float* acc_dst, const int32_t* new_lens, const int32_t* kept) {
-    if (!acc || !p || !new_lens || !kept) return SBA_ERR_INVALID_ARG;
+    if (!acc || !aligned16(acc) || !p || !new_lens || !kept) return SBA_ERR_INVALID_ARG;
     if (p->n_keep < 1 || p->n_sink < 0 || p->n_recent < 0 || (int64_t)p->n_sink + p->n_recent > p->n_keep)
         return SBA_ERR_INVALID_ARG;
     if (dst.B != src.B || dst.H_kv != src.H_kv || dst.b != src.b) return SBA_ERR_INVALID_ARG;

@@ -4,16 +4,18 @@
 // heaviest, up to n_keep in all (weight descending, then position ascending; -0 == +0, a NaN ranks
 // below every number).  Kept tokens stay in order, so "recent" and the local blocks of later steps
 // mean what they meant.  Two launches:
-//  - evict_select_kernel: one thread-block cluster per (sequence, KV head).  The threshold is found by
-//    a radix select, 8 bits of the order-preserving key a pass: every CTA histograms its slice of the
-//    weights in shared memory, and all CTAs add the cluster's histograms through distributed shared
-//    memory, so each pass is one cluster barrier.  The slice is read from L2 (or L1) again each pass:
-//    4 bytes a token.  Two more passes count and write the kept positions, in order, without atomics.
-//    It is bound by the latency of its dependent passes.
+//  - evict_select_kernel: one thread-block cluster per (sequence, KV head).  Every CTA reads its
+//    slice of the weights once, four tokens a load, and keeps their order-preserving 32-bit keys in
+//    shared memory (as far as they fit; the rest is read again from L2).  The threshold is found by a
+//    radix select of 11, 11 and 10 bits: a shared-memory histogram of the slice, then one cluster
+//    barrier, after which every CTA adds the cluster's histograms through distributed shared memory
+//    and finds the same digit.  A count and an ordered write follow; no position depends on an atomic.
 //  - gather kernels: one CTA per (destination block, KV head, sequence) moves the rows (whole rows,
 //    16 bytes a lane, all loads of a thread issued before its first store), the accumulators, and forms the
 //    block's Quest descriptor from the keys it holds in registers.  Bound by HBM.
 #include <math.h>
+
+#include <mutex>
 
 #include "common.cuh"
 #include "kv4.cuh"
@@ -23,9 +25,12 @@ namespace sba {
 
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kMaxCluster = 8;  // the portable cluster size
+constexpr int kMaxCluster = 16;
+constexpr int kBins = 2048;
+constexpr int kSelFixed = 2 * kBins * 4;          // two histograms
+constexpr int kSelMaxKeys = 200 * 1024 / 4;       // keys of a slice kept in shared memory
 constexpr int kMoveThreads = 256;
 
 struct SelectArgs {
@@ -43,17 +48,18 @@ __device__ __forceinline__ int clamped_len(const int32_t* seq_lens, int s, int m
     return max(0, min(__ldca(seq_lens + s), max_blocks * b));
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a) {
-    __shared__ uint32_t hist[4][256];
-    __shared__ uint32_t scan[8];
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a, int cap) {
+    extern __shared__ __align__(16) uint32_t dyn[];
+    uint32_t* keys = dyn + 2 * kBins;
+    __shared__ uint32_t scan[kSelWarps];
     __shared__ uint32_t found[2];  // digit of the threshold, tokens still to take at it
-    __shared__ uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
-    __shared__ uint32_t totals[2];  // tokens of this CTA above and at the threshold
+    __shared__ uint2 warp_n[kSelWarps];
+    __shared__ uint2 total;  // tokens of this CTA above and at the threshold
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, s = blockIdx.z;
     const uint32_t rank = cluster_rank(), C = cluster_size();
-    for (int i = tid; i < 4 * 256; i += kSelThreads) hist[i >> 8][i & 255] = 0;
+    for (int i = tid; i < 2 * kBins; i += kSelThreads) dyn[i] = 0;
     pdl_wait();
     pdl_trigger();
     const int n = clamped_len(a.seq_lens, s, a.max_blocks, a.b);
@@ -64,107 +70,160 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(SelectArgs a)
         for (int i = (int)rank * kSelThreads + tid; i < n; i += (int)C * kSelThreads) kept[i] = i;
         return;
     }
-    const int sink = a.p.n_sink, recent = a.p.n_recent, k = keep - sink - recent;
+    const int sink = a.p.n_sink, last = n - a.p.n_recent, k = keep - sink - a.p.n_recent;  // ranked: [sink, last)
     for (int i = (int)rank * kSelThreads + tid; i < sink; i += (int)C * kSelThreads) kept[i] = i;
-    for (int i = (int)rank * kSelThreads + tid; i < recent; i += (int)C * kSelThreads)
-        kept[keep - recent + i] = n - recent + i;
+    for (int i = (int)rank * kSelThreads + tid; i < n - last; i += (int)C * kSelThreads)
+        kept[keep - (n - last) + i] = last + i;
     if (k == 0) return;
 
-    // this CTA's slice [lo, hi) of the ranked tokens, and this warp's part of it
-    const int64_t m = n - recent - sink;
-    const int lo = sink + (int)(m * rank / C), hi = sink + (int)(m * (rank + 1) / C);
-    const int wlo = lo + (int)((int64_t)(hi - lo) * warp / kSelWarps);
-    const int whi = lo + (int)((int64_t)(hi - lo) * (warp + 1) / kSelWarps);
-    auto key_of = [&](int t) -> uint32_t {
-        const int j = t / a.b;
+    // this CTA's slice: quads of tokens [q0, q0 + nq)
+    const int n4 = (n + 3) / 4;
+    const int q0 = (int)((int64_t)n4 * rank / C), nq = (int)((int64_t)n4 * (rank + 1) / C) - q0;
+    // keys of quad i of the slice: 0 outside the ranked tokens, 1 for a NaN, larger for a larger weight
+    auto read_quad = [&](int i) -> uint4 {
+        const int t = 4 * (q0 + i), j = t / a.b;
         const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
-        if (page < 0) return 0u;
-        const float w = __ldca(a.acc + (page * a.H_kv + h) * a.b + (t - j * a.b));
-        return w != w ? 0u : orderable_key(w);
+        float4 w = make_float4(NAN, NAN, NAN, NAN);  // a bad page's tokens rank last
+        if (page >= 0) w = __ldca(reinterpret_cast<const float4*>(a.acc + (page * a.H_kv + h) * a.b + (t - j * a.b)));
+        uint4 r;
+        r.x = t < sink || t >= last ? 0u : w.x != w.x ? 1u : orderable_key(w.x);
+        r.y = t + 1 < sink || t + 1 >= last ? 0u : w.y != w.y ? 1u : orderable_key(w.y);
+        r.z = t + 2 < sink || t + 2 >= last ? 0u : w.z != w.z ? 1u : orderable_key(w.z);
+        r.w = t + 3 < sink || t + 3 >= last ? 0u : w.w != w.w ? 1u : orderable_key(w.w);
+        return r;
+    };
+    auto quad = [&](int i) -> uint4 {
+        return 4 * i < cap ? *reinterpret_cast<const uint4*>(keys + 4 * i) : read_quad(i);
     };
 
     __syncthreads();
+    // ---- read the slice; histogram of the top 11 bits ----
+    for (int i0 = tid; i0 < nq; i0 += 4 * kSelThreads) {
+        uint4 r[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (i0 + x * kSelThreads < nq) r[x] = read_quad(i0 + x * kSelThreads);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int i = i0 + x * kSelThreads;
+            if (i >= nq) break;
+            if (4 * i < cap) *reinterpret_cast<uint4*>(keys + 4 * i) = r[x];
+            if (r[x].x) atomicAdd(&dyn[r[x].x >> 21], 1u);
+            if (r[x].y) atomicAdd(&dyn[r[x].y >> 21], 1u);
+            if (r[x].z) atomicAdd(&dyn[r[x].z >> 21], 1u);
+            if (r[x].w) atomicAdd(&dyn[r[x].w >> 21], 1u);
+        }
+    }
     uint32_t prefix = 0, left = (uint32_t)k;  // left: tokens to take among those whose key starts with prefix
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int t0 = wlo; t0 < whi; t0 += 32) {
-            const int t = t0 + lane;
-            const uint32_t key = t < whi ? key_of(t) : 0u;
-            const bool in = t < whi && (pass == 0 || (key >> (shift + 8)) == prefix);
-            const uint32_t digit = in ? (key >> shift) & 255u : 256u;
-            const uint32_t same = __match_any_sync(0xffffffffu, digit);
-            if (in && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&hist[pass][digit], (uint32_t)__popc(same));
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+        uint32_t* hist = dyn + (pass & 1) * kBins;
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 0 : shift + 11 - (pass == 2);
+        if (pass > 0) {
+            for (int i = tid; i < nq; i += kSelThreads) {
+                const uint4 r = quad(i);
+                const uint32_t mask = pass == 1 ? 2047u : 1023u;
+                if (r.x >> top == prefix && r.x) atomicAdd(&hist[(r.x >> shift) & mask], 1u);
+                if (r.y >> top == prefix && r.y) atomicAdd(&hist[(r.y >> shift) & mask], 1u);
+                if (r.z >> top == prefix && r.z) atomicAdd(&hist[(r.z >> shift) & mask], 1u);
+                if (r.w >> top == prefix && r.w) atomicAdd(&hist[(r.w >> shift) & mask], 1u);
+            }
         }
         cluster_sync();
-        // digits from the top: thread d looks at digit 255 - d
-        uint32_t c = 0, below = 0;
-        if (tid < 256) {
-            for (uint32_t r = 0; r < C; ++r) c += ld_peer_u32(peer_addr(&hist[pass][255 - tid], r));
-            uint32_t sum = c;
+        if (pass == 1)  // every CTA has read the first histogram
+            for (int i = tid; i < kBins; i += kSelThreads) dyn[i] = 0;
+        // digits from the top: thread t takes bins kBins - 1 - 2t and the one below
+        uint32_t hi = 0, lo = 0;
+        const int bin = kBins - 2 - 2 * tid;
+        for (uint32_t r = 0; r < C; ++r) {
+            const uint32_t at = peer_addr(&hist[bin], r);
+            lo += ld_peer_u32(at);
+            hi += ld_peer_u32(at + 4);
+        }
+        uint32_t sum = hi + lo;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += v;
-            }
-            if (lane == 31) scan[warp] = sum;
-            below = sum - c;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) scan[warp] = sum;
+        __syncthreads();
+        uint32_t before = lane < warp ? scan[lane] : 0u;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        before += sum - hi - lo;  // tokens in higher bins
+        if (before < left && before + hi >= left) {
+            found[0] = bin + 1;
+            found[1] = left - before;
+        } else if (before + hi < left && before + hi + lo >= left) {
+            found[0] = bin;
+            found[1] = left - before - hi;
         }
         __syncthreads();
-        if (tid < 256) {
-            for (int w = 0; w < warp; ++w) below += scan[w];
-            if (below < left && below + c >= left) {
-                found[0] = 255 - tid;
-                found[1] = left - below;
-            }
-        }
-        __syncthreads();
-        prefix = (prefix << 8) | found[0];
+        prefix = (prefix << (pass == 2 ? 10 : 11)) | found[0];
         left = found[1];
         __syncthreads();
     }
     const uint32_t T = prefix;
 
-    // tokens above and at the threshold: per warp, per CTA, then the CTAs before this one
+    // ---- tokens above and at the threshold: per warp (a run of quads each), per CTA, then the CTAs before ----
+    const int w0 = (int)((int64_t)nq * warp / kSelWarps), w1 = (int)((int64_t)nq * (warp + 1) / kSelWarps);
     uint32_t gt = 0, eq = 0;
-    for (int t0 = wlo; t0 < whi; t0 += 32) {
-        const int t = t0 + lane;
-        const uint32_t key = t < whi ? key_of(t) : 0u;
-        gt += __popc(__ballot_sync(0xffffffffu, t < whi && key > T));
-        eq += __popc(__ballot_sync(0xffffffffu, t < whi && key == T));
+    for (int i = w0 + lane; i < w1; i += 32) {
+        const uint4 r = quad(i);
+        gt += (r.x > T) + (r.y > T) + (r.z > T) + (r.w > T);
+        eq += (r.x == T) + (r.y == T) + (r.z == T) + (r.w == T);
     }
-    if (lane == 0) {
-        warp_gt[warp] = gt;
-        warp_eq[warp] = eq;
-    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) warp_n[warp] = make_uint2(gt, eq);
     __syncthreads();
-    if (tid == 0) {
-        uint32_t g = 0, e = 0;
-        for (int w = 0; w < kSelWarps; ++w) {
-            const uint32_t gw = warp_gt[w], ew = warp_eq[w];
-            warp_gt[w] = g;
-            warp_eq[w] = e;
-            g += gw;
-            e += ew;
+    if (warp == 0) {  // exclusive sums over the warps
+        const uint2 mine = warp_n[lane];
+        uint32_t g = mine.x, e = mine.y;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t vg = __shfl_up_sync(0xffffffffu, g, o), ve = __shfl_up_sync(0xffffffffu, e, o);
+            if (lane >= o) {
+                g += vg;
+                e += ve;
+            }
         }
-        totals[0] = g;
-        totals[1] = e;
+        warp_n[lane] = make_uint2(g - mine.x, e - mine.y);
+        if (lane == 31) total = make_uint2(g, e);
     }
     cluster_sync();
-    uint32_t g0 = warp_gt[warp], e0 = warp_eq[warp];
-    for (uint32_t r = 0; r < rank; ++r) {
-        g0 += ld_peer_u32(peer_addr(&totals[0], r));
-        e0 += ld_peer_u32(peer_addr(&totals[1], r));
+    uint32_t g0 = 0, e0 = 0;
+    if (lane < rank) {
+        g0 = ld_peer_u32(peer_addr(&total.x, lane));
+        e0 = ld_peer_u32(peer_addr(&total.y, lane));
     }
-    const uint32_t lower = (1u << lane) - 1u;
-    for (int t0 = wlo; t0 < whi; t0 += 32) {
-        const int t = t0 + lane;
-        const uint32_t key = t < whi ? key_of(t) : 0u;
-        const bool is_gt = t < whi && key > T, is_eq = t < whi && key == T;
-        const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-        const uint32_t my_e = e0 + __popc(be & lower), my_g = g0 + __popc(bg & lower);
-        if (is_gt || (is_eq && my_e < left)) kept[sink + my_g + min(my_e, left)] = t;
-        g0 += __popc(bg);
-        e0 += __popc(be);
+    g0 = __reduce_add_sync(0xffffffffu, g0) + warp_n[warp].x;
+    e0 = __reduce_add_sync(0xffffffffu, e0) + warp_n[warp].y;
+    for (int i0 = w0; i0 < w1; i0 += 32) {
+        const int i = i0 + lane;
+        const uint4 r = i < w1 ? quad(i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+        uint32_t mine = 0;  // tokens above in the low half, at the threshold in the high half
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mine += (v[x] > T ? 1u : 0u) + (v[x] == T ? 0x10000u : 0u);
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        uint32_t g = g0 + ((upto - mine) & 0xffffu), e = e0 + ((upto - mine) >> 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const bool above = v[x] > T, at = v[x] == T;
+            if (above || (at && e < left)) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
+            g += above;
+            e += at;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        g0 += all & 0xffffu;
+        e0 += all >> 16;
     }
     cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
@@ -355,24 +414,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kv4_kernel(MoveArgs a
     }
 }
 
-// One cluster per (sequence, KV head): as many CTAs as fill the GPU, and as have 2048 tokens each.
-int select_cluster(int64_t units, int max_len) {
-    int C = 1;
-    while (C < kMaxCluster && units * C * 2 <= 148 && max_len / (2 * C) >= 2048) C *= 2;
-    return C;
-}
-
-template <class Cache>
-int launch_select(const Cache& src, const float* acc, const sba_evict_params& p, int32_t* new_lens, int32_t* kept,
-                  cudaStream_t stream) {
-    SelectArgs a{src.seq_lens, src.block_table, src.status, src.H_kv, src.b, src.max_blocks, src.num_pages, acc, p, kept,
-                 new_lens};
-    const int C = select_cluster((int64_t)src.B * src.H_kv, src.max_len);
+cudaLaunchConfig_t select_config(int C, int H_kv, int B, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C, src.H_kv, src.B);
+    cfg.gridDim = dim3(C, H_kv, B);
     cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = C;
     attr[0].val.clusterDim.y = 1;
@@ -381,7 +428,58 @@ int launch_select(const Cache& src, const float* acc, const sba_evict_params& p,
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    return cfg;
+}
+
+// Clusters of C CTAs (one CTA per SM) that the current device keeps resident at once; asked once per
+// device and size.
+int resident_clusters(int C) {
+    static std::mutex lock;
+    static int known[64][kMaxCluster + 1] = {};  // answer + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> hold(lock);
+    if (known[dev][0] == 0) {
+        if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return 0;
+        known[dev][0] = 1;
+    }
+    if (known[dev][C] == 0) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = select_config(C, 1, 1, kSelFixed + kSelMaxKeys * 4, nullptr, attr);
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, evict_select_kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        known[dev][C] = n + 1;
+    }
+    return known[dev][C] - 1;
+}
+
+// CTAs per (sequence, KV head): the most whose clusters are all resident at once, with 4096 tokens a
+// CTA at least (a smaller slice costs less than the larger cluster's barriers); one if the units
+// alone fill the GPU.
+int select_cluster(int64_t units, int max_len) {
+    int most = max_len / 4096;
+    if (most > kMaxCluster) most = kMaxCluster;
+    for (int C = most; C > 1; --C)
+        if (units * C <= 148 && resident_clusters(C) >= units) return C;
+    return 1;
+}
+
+template <class Cache>
+int launch_select(const Cache& src, const float* acc, const sba_evict_params& p, int32_t* new_lens, int32_t* kept,
+                  cudaStream_t stream) {
+    SelectArgs a{src.seq_lens, src.block_table, src.status, src.H_kv, src.b, src.max_blocks, src.num_pages, acc, p, kept,
+                 new_lens};
+    if (allow_smem<evict_select_kernel>(kSelFixed + kSelMaxKeys * 4) != SBA_OK) return SBA_ERR_CUDA;
+    const int C = select_cluster((int64_t)src.B * src.H_kv, src.max_len);
+    const int64_t slice = (((int64_t)src.max_len + 3) / 4 + C - 1) / C * 4;
+    const int cap = (int)(slice < kSelMaxKeys ? slice : kSelMaxKeys);
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = select_config(C, src.H_kv, src.B, kSelFixed + cap * 4, stream, attr);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, cap);
     if (e != cudaSuccess) {
         note_cuda_error(e);
         return SBA_ERR_CUDA;

@@ -497,9 +497,9 @@ int sba_accumulate_weights_kv4(const sba_cache4 *c, const void *q, int32_t M, co
                                const float *acc_in, float *acc_out, void *stream);
 
 /* Evict: every (sequence, KV head) of `src` keeps min(len_s, n_keep) tokens -- the first n_sink, the
- * last n_recent and the heaviest of the others by `acc` (fp32 [num_pages][H_kv][b] of src; weight
- * descending, then position ascending; -0 == +0; a NaN ranks below every number) -- and their K/V rows
- * are copied, in order, to positions 0, 1, ... of `dst`.  The keys must carry their position
+ * last n_recent and the heaviest of the others by `acc` (fp32 [num_pages][H_kv][b] of src, 16-byte
+ * aligned; weight descending, then position ascending; -0 == +0; a NaN ranks below every number) -- and
+ * their K/V rows are copied, in order, to positions 0, 1, ... of `dst`.  The keys must carry their position
  * themselves (rotary embeddings applied before caching), since a token's slot changes.
  * dst        a cache of the same B, H_kv and b whose pages are not pages of src (the same pool with
  *            another block table, or another pool); n_keep <= dst->max_blocks * b.  dst->seq_lens is not

@@ -190,7 +190,7 @@ def test_bad_evict():
         return lib.sba_evict(src or c16(), acc, ctypes.byref(sba.evict_params(*p)),
                              dst or c16(k=0x100000, v=0x200000, desc=None), acc_dst, new, kept, None)
 
-    assert call(acc=None) == ARG and call(new=None) == ARG and call(kept=None) == ARG
+    assert call(acc=None) == ARG and call(acc=0x5008) == ARG and call(new=None) == ARG and call(kept=None) == ARG
     assert call(p=(0, 0, 0)) == ARG and call(p=(64, -1, 0)) == ARG and call(p=(64, 0, -1)) == ARG
     assert call(p=(64, 33, 32)) == ARG and call(p=(64, 2 ** 31 - 1, 2 ** 31 - 1)) == ARG
     assert call(p=(4097, 0, 0)) == ARG                                                  # dst has room for 4096
