@@ -30,14 +30,14 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kBins = 2048;
 constexpr int kSelFixed = 2 * kBins * 4;          // two histograms
-constexpr int kSelMaxKeys = 200 * 1024 / 4;       // keys of a slice kept in shared memory
+constexpr int kSelMaxKeys = (226 * 1024 - kSelFixed) / 4;  // keys of a slice kept in shared memory
 constexpr int kMoveThreads = 256;
 
 struct SelectArgs {
     const int32_t* seq_lens;
     const int32_t* block_table;
     int32_t* status;
-    int H_kv, b, max_blocks, num_pages;
+    int H_kv, b, log2_b, max_blocks, num_pages;
     const float* acc;
     sba_evict_params p;
     int32_t* kept;
@@ -46,6 +46,10 @@ struct SelectArgs {
 
 __device__ __forceinline__ int clamped_len(const int32_t* seq_lens, int s, int max_blocks, int b) {
     return max(0, min(__ldca(seq_lens + s), max_blocks * b));
+}
+
+__device__ __forceinline__ void ld_peer_v2(uint32_t addr, uint32_t& a, uint32_t& b) {
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a, int cap) {
@@ -81,7 +85,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     const int q0 = (int)((int64_t)n4 * rank / C), nq = (int)((int64_t)n4 * (rank + 1) / C) - q0;
     // keys of quad i of the slice: 0 outside the ranked tokens, 1 for a NaN, larger for a larger weight
     auto read_quad = [&](int i) -> uint4 {
-        const int t = 4 * (q0 + i), j = t / a.b;
+        const int t = 4 * (q0 + i), j = t >> a.log2_b;
         const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
         float4 w = make_float4(NAN, NAN, NAN, NAN);  // a bad page's tokens rank last
         if (page >= 0) w = __ldca(reinterpret_cast<const float4*>(a.acc + (page * a.H_kv + h) * a.b + (t - j * a.b)));
@@ -98,13 +102,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
 
     __syncthreads();
     // ---- read the slice; histogram of the top 11 bits ----
-    for (int i0 = tid; i0 < nq; i0 += 4 * kSelThreads) {
-        uint4 r[4];
+    constexpr int kLoads = 8;  // in flight per thread
+    for (int i0 = tid; i0 < nq; i0 += kLoads * kSelThreads) {
+        uint4 r[kLoads];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < kLoads; ++x)
             if (i0 + x * kSelThreads < nq) r[x] = read_quad(i0 + x * kSelThreads);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < kLoads; ++x) {
             const int i = i0 + x * kSelThreads;
             if (i >= nq) break;
             if (4 * i < cap) *reinterpret_cast<uint4*>(keys + 4 * i) = r[x];
@@ -120,9 +125,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         uint32_t* hist = dyn + (pass & 1) * kBins;
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 0 : shift + 11 - (pass == 2);
         if (pass > 0) {
+            const uint32_t mask = pass == 1 ? 2047u : 1023u;
+#pragma unroll 4
             for (int i = tid; i < nq; i += kSelThreads) {
                 const uint4 r = quad(i);
-                const uint32_t mask = pass == 1 ? 2047u : 1023u;
                 if (r.x >> top == prefix && r.x) atomicAdd(&hist[(r.x >> shift) & mask], 1u);
                 if (r.y >> top == prefix && r.y) atomicAdd(&hist[(r.y >> shift) & mask], 1u);
                 if (r.z >> top == prefix && r.z) atomicAdd(&hist[(r.z >> shift) & mask], 1u);
@@ -135,10 +141,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         // digits from the top: thread t takes bins kBins - 1 - 2t and the one below
         uint32_t hi = 0, lo = 0;
         const int bin = kBins - 2 - 2 * tid;
-        for (uint32_t r = 0; r < C; ++r) {
-            const uint32_t at = peer_addr(&hist[bin], r);
-            lo += ld_peer_u32(at);
-            hi += ld_peer_u32(at + 4);
+        uint32_t c[kMaxCluster][2];  // all loads before the first sum
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            c[r][0] = c[r][1] = 0;
+            if (r < C) ld_peer_v2(peer_addr(&hist[bin], r), c[r][0], c[r][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            lo += c[r][0];
+            hi += c[r][1];
         }
         uint32_t sum = hi + lo;
 #pragma unroll
@@ -169,6 +181,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     // ---- tokens above and at the threshold: per warp (a run of quads each), per CTA, then the CTAs before ----
     const int w0 = (int)((int64_t)nq * warp / kSelWarps), w1 = (int)((int64_t)nq * (warp + 1) / kSelWarps);
     uint32_t gt = 0, eq = 0;
+#pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
         const uint4 r = quad(i);
         gt += (r.x > T) + (r.y > T) + (r.z > T) + (r.w > T);
@@ -200,30 +213,29 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     }
     g0 = __reduce_add_sync(0xffffffffu, g0) + warp_n[warp].x;
     e0 = __reduce_add_sync(0xffffffffu, e0) + warp_n[warp].y;
+    const uint32_t lower = (1u << lane) - 1u;
     for (int i0 = w0; i0 < w1; i0 += 32) {
         const int i = i0 + lane;
         const uint4 r = i < w1 ? quad(i) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t v[4] = {r.x, r.y, r.z, r.w};
-        uint32_t mine = 0;  // tokens above in the low half, at the threshold in the high half
-#pragma unroll
-        for (int x = 0; x < 4; ++x) mine += (v[x] > T ? 1u : 0u) + (v[x] == T ? 0x10000u : 0u);
-        uint32_t upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
-        uint32_t g = g0 + ((upto - mine) & 0xffffu), e = e0 + ((upto - mine) >> 16);
+        uint32_t above[4], at[4], all_g = 0, all_e = 0, g = g0, e = e0;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const bool above = v[x] > T, at = v[x] == T;
-            if (above || (at && e < left)) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
-            g += above;
-            e += at;
+            above[x] = __ballot_sync(0xffffffffu, v[x] > T);
+            at[x] = __ballot_sync(0xffffffffu, v[x] == T);
+            g += __popc(above[x] & lower);
+            e += __popc(at[x] & lower);
+            all_g += __popc(above[x]);
+            all_e += __popc(at[x]);
         }
-        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
-        g0 += all & 0xffffu;
-        e0 += all >> 16;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (v[x] > T || (v[x] == T && e < left)) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
+            g += v[x] > T;
+            e += v[x] == T;
+        }
+        g0 += all_g;
+        e0 += all_e;
     }
     cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
@@ -249,15 +261,20 @@ struct MoveArgs {
 template <int kBlk>
 __device__ __forceinline__ int source_rows(const MoveArgs& a, int64_t* src, int64_t& dst_page) {
     const int jd = blockIdx.x, h = blockIdx.y, s = blockIdx.z, tid = threadIdx.x;
+    // the position, the length and the destination page do not wait for one another
+    const bool in = tid < kBlk && jd * kBlk + tid < a.n_keep;
+    const int t = in ? __ldca(a.kept + ((int64_t)s * a.H_kv + h) * a.n_keep + jd * kBlk + tid) : 0;
+    dst_page = page_of(a.dst_table, a.dst_max_blocks, a.dst_pages, s, jd, nullptr);
     const int n = clamped_len(a.seq_lens, s, a.src_max_blocks, kBlk);
     const int rows = min(kBlk, min(n, a.n_keep) - jd * kBlk);
     if (rows <= 0) return 0;
-    dst_page = page_of(a.dst_table, a.dst_max_blocks, a.dst_pages, s, jd, tid == 0 ? a.dst_status : nullptr);
-    if (dst_page < 0) return 0;
+    if (dst_page < 0) {
+        if (tid == 0) report(a.dst_status, SBA_DEV_BAD_PAGE);
+        return 0;
+    }
     if (tid < kBlk) {
         int64_t from = -1;
         if (tid < rows) {
-            const int t = __ldca(a.kept + ((int64_t)s * a.H_kv + h) * a.n_keep + jd * kBlk + tid);
             const int64_t page = page_of(a.src_table, a.src_max_blocks, a.src_pages, s, t / kBlk, a.status);
             if (page >= 0) from = (page * a.H_kv + h) * kBlk + t % kBlk;
         }
@@ -338,10 +355,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(MoveArgs a) {
     }
 }
 
-// Four-bit cache: 8 lanes move a row, four for the key codes and four for the value codes (16 bytes each), every lane
-// also two scales of its own 32 channels, so a key lane can form the descriptor from what it moves.
+// Four-bit cache: 8 lanes move a row, four for the key codes and four for the value codes (16 bytes
+// each), every lane also the two scales of its own 32 channels.  For the descriptor the value lanes
+// take the upper half of a key lane's channels: 16 channels a lane keep the registers few, so that
+// eight CTAs share an SM (the kernel waits for its three dependent loads, not for bandwidth).
 template <int kBlk>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kv4_kernel(MoveArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, kBlk == 64 ? 8 : 6) evict_move_kv4_kernel(MoveArgs a) {
     constexpr int kIter = kBlk / 32;
     __shared__ int64_t src[kBlk];
     __shared__ uint32_t red[2][kMoveThreads / 32][64];
@@ -357,51 +376,57 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kv4_kernel(MoveArgs a
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
         const int64_t from = src[r + 32 * i];
+        code[i] = make_uint4(0u, 0u, 0u, 0u);
+        sc[i] = 0;
         if (from >= 0) {
             const uint8_t* strip = a.k_src + (from >> 5) * kStripBytes;
             code[i] = ld_once_v4(strip + (from & 31) * 64 + codes_at);
             sc[i] = __ldca(reinterpret_cast<const uint16_t*>(strip + (from & 31) * 8 + scales_at));
         }
     }
-    __half2 mn[16], mx[16];
+    __half2 mn[8], mx[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 8; ++e) {
         mn[e] = __half2half2(__ushort_as_half(0x7c00));
         mx[e] = __half2half2(__ushort_as_half(0xfc00));
     }
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        if (src[r + 32 * i] < 0) continue;
-        uint8_t* strip = tile + i * kStripBytes;
-        *reinterpret_cast<uint4*>(strip + r * 64 + codes_at) = code[i];
-        *reinterpret_cast<uint16_t*>(strip + r * 8 + scales_at) = (uint16_t)sc[i];
-        if (a.desc && g < 4) {
-            const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+        const bool real = src[r + 32 * i] >= 0;
+        if (real) {
+            uint8_t* strip = tile + i * kStripBytes;
+            *reinterpret_cast<uint4*>(strip + r * 64 + codes_at) = code[i];
+            *reinterpret_cast<uint16_t*>(strip + r * 8 + scales_at) = (uint16_t)sc[i];
+        }
+        if (a.desc) {  // channels 32(g % 4) + 16(g / 4) ..: the key lane's words x, y or z, w
+            const uint32_t z = __shfl_sync(0xffffffffu, code[i].z, lane & ~4), w = __shfl_sync(0xffffffffu, code[i].w, lane & ~4);
+            const uint32_t ks = __shfl_sync(0xffffffffu, sc[i], lane & ~4);
+            uint32_t v[8];
+            codes_to_f16(g < 4 ? code[i].x : z, v[0], v[1], v[2], v[3]);
+            codes_to_f16(g < 4 ? code[i].y : w, v[4], v[5], v[6], v[7]);
+            const uint32_t f = scale_f16x2(g < 4 ? ks & 0xffu : ks >> 8);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t v[4];
-                codes_to_f16(w[x], v[0], v[1], v[2], v[3]);
-                const uint32_t f = scale_f16x2(x < 2 ? sc[i] & 0xffu : sc[i] >> 8);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t y = mul_f16x2(v[e], f);
-                    mn[4 * x + e] = __hmin2(mn[4 * x + e], *reinterpret_cast<const __half2*>(&y));
-                    mx[4 * x + e] = __hmax2(mx[4 * x + e], *reinterpret_cast<const __half2*>(&y));
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t y = mul_f16x2(v[e], f);
+                if (real) {
+                    mn[e] = __hmin2(mn[e], *reinterpret_cast<const __half2*>(&y));
+                    mx[e] = __hmax2(mx[e], *reinterpret_cast<const __half2*>(&y));
                 }
             }
         }
     }
     if (!a.desc) return;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 8; ++e) {
 #pragma unroll
         for (int o = 8; o < 32; o <<= 1) {
             mn[e] = __hmin2(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], o));
             mx[e] = __hmax2(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
         }
-        if (lane < 4) {
-            red[0][warp][g * 16 + e] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&mn[e]));
-            red[1][warp][g * 16 + e] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&mx[e]));
+        if (lane < 8) {
+            const int pair = (g & 3) * 16 + (g >> 2) * 8 + e;
+            red[0][warp][pair] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&mn[e]));
+            red[1][warp][pair] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&mx[e]));
         }
     }
     __syncthreads();
@@ -471,7 +496,7 @@ int select_cluster(int64_t units, int max_len) {
 template <class Cache>
 int launch_select(const Cache& src, const float* acc, const sba_evict_params& p, int32_t* new_lens, int32_t* kept,
                   cudaStream_t stream) {
-    SelectArgs a{src.seq_lens, src.block_table, src.status, src.H_kv, src.b, src.max_blocks, src.num_pages, acc, p, kept,
+    SelectArgs a{src.seq_lens, src.block_table, src.status, src.H_kv, src.b, src.b == 64 ? 6 : 7, src.max_blocks, src.num_pages, acc, p, kept,
                  new_lens};
     if (allow_smem<evict_select_kernel>(kSelFixed + kSelMaxKeys * 4) != SBA_OK) return SBA_ERR_CUDA;
     const int C = select_cluster((int64_t)src.B * src.H_kv, src.max_len);
