@@ -458,66 +458,69 @@ class Cache4:
                self.max_blocks, self.max_len)
         cached = self.__dict__.get("_struct")
         if cached is None or cached[0] != key:
-            dev = self.kv.device
             if self.kv.dim() != 4 or self.kv.shape[3] != STRIP_BYTES:
                 raise ValueError(f"kv must be uint8 [num_pages][H_kv][b/32][{STRIP_BYTES}]")
-            _tensor(self.seq_lens, torch.int32, dev, self.B, "seq_lens")
-            _tensor(self.block_table, torch.int32, dev, self.B * self.max_blocks, "block_table")
-            _tensor(self.desc, torch.bfloat16, dev, self.num_pages * self.H_kv * 2 * self.d, "desc")
-            _tensor(self.status, torch.int32, dev, 1, "status")
-            st = sba_cache4(_tensor(self.kv, torch.uint8, dev, 0, "kv"), _ptr(self.block_table), _ptr(self.seq_lens),
-                            self.B, self.H_q, self.H_kv, self.d, self.b, self.max_blocks, self.num_pages, self.max_len,
-                            _ptr(self.desc), _ptr(self.status))
-            # the tensors themselves stay in the key's reach, so that an id is not met again on another one
-            cached = (key, st, ctypes.byref(st), (self.kv, self.block_table, self.seq_lens, self.desc, self.status))
+            if not self.kv.is_cuda:
+                raise ValueError("libsba takes device tensors only")
+            dev = self.kv.get_device()
+            st = sba_cache4(_tensor(self.kv, torch.uint8, dev, 0, "kv"),
+                            _tensor(self.block_table, torch.int32, dev, self.B * self.max_blocks, "block_table"),
+                            _tensor(self.seq_lens, torch.int32, dev, self.B, "seq_lens"), self.B, self.H_q, self.H_kv,
+                            self.d, self.b, self.max_blocks, self.num_pages, self.max_len,
+                            _tensor(self.desc, torch.bfloat16, dev, self.num_pages * self.H_kv * 2 * self.d, "desc"),
+                            _tensor(self.status, torch.int32, dev, 1, "status"))
+            # the tensors stay alive beside the key, so that an id is not met again on another one
+            cached = (key, st, (self.kv, self.block_table, self.seq_lens, self.desc, self.status))
             self.__dict__["_struct"] = cached
         return cached[1]
 
 
-def _tensor(t: Optional[torch.Tensor], dtype: torch.dtype, device: torch.device, least: int, name: str):
-    """Pointer of a contiguous tensor of `dtype` on `device` with at least `least` elements (None stays None)."""
+def _tensor(t: Optional[torch.Tensor], dtype: torch.dtype, device: int, least: int, name: str):
+    """Address of a contiguous tensor of `dtype` on CUDA device `device` with at least `least` elements
+    (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() < least:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on {device} with at least {least} elements "
-                         f"(got {t.dtype} on {t.device}, {t.numel()} elements"
-                         f"{'' if t.is_contiguous() else ', not contiguous'})")
-    return t.data_ptr()
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous() and t.numel() >= least:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{device} with at least {least} elements "
+                     f"(got {t.dtype} on {t.device}, {t.numel()} elements"
+                     f"{'' if t.is_contiguous() else ', not contiguous'})")
 
 
-def _current(device: torch.device, stream):
+def _current(device: int, stream):
     """The stream to launch on; kernels run on the current device, so the tensors have to be there."""
-    if device.type != "cuda":
-        raise ValueError("libsba takes device tensors only")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return _stream(stream)
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on cuda:{device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
 
 
-def _device_of(c) -> torch.device:
-    return c.kv.device if isinstance(c, Cache4) else c.k.device
+def _opened(c):
+    """A cache's struct (by reference), itself, and its device."""
+    st = c.struct()
+    t = c.kv if type(c) is Cache4 else c.k
+    return ctypes.byref(st), st, t.get_device()
 
 
-def _rows_of(c, q: torch.Tensor):
-    """Pointer of q ([B][H_q][d], or [B][M][H_q][d]) and M."""
-    M = int(q.shape[1]) if q.dim() == 4 else 1
-    want = (c.B, M, c.H_q, c.d) if q.dim() == 4 else (c.B, c.H_q, c.d)
-    if tuple(q.shape) != want:
-        raise ValueError(f"q must be [B][H_q][d] or [B][M][H_q][d] (got {tuple(q.shape)} for {want})")
-    return _tensor(q, torch.bfloat16, _device_of(c), 0, "q"), M
+def _rows_of(st, device: int, q: torch.Tensor):
+    """Address of q ([B][H_q][d], or [B][M][H_q][d]) and M."""
+    shape = q.shape
+    M = shape[1] if len(shape) == 4 else 1
+    if shape != ((st.B, M, st.H_q, st.d) if len(shape) == 4 else (st.B, st.H_q, st.d)):
+        raise ValueError(f"q must be [B][H_q][d] or [B][M][H_q][d] (got {tuple(shape)})")
+    return _tensor(q, torch.bfloat16, device, 0, "q"), M
 
 
-def _selection(c, sel_idx, sel_cnt):
-    """Pointers of a selection and its row length (None, None, 0: every block)."""
+def _selection(st, device: int, sel_idx, sel_cnt):
+    """Addresses of a selection and its row length (None, None, 0: every block)."""
     if sel_idx is None:
         if sel_cnt is not None:
             raise ValueError("sel_cnt without sel_idx")
         return None, None, 0
-    if sel_cnt is None or sel_idx.dim() != 3 or tuple(sel_idx.shape[:2]) != (c.B, c.H_kv):
+    shape = sel_idx.shape
+    if sel_cnt is None or len(shape) != 3 or shape[0] != st.B or shape[1] != st.H_kv:
         raise ValueError("sel_idx must be int32 [B][H_kv][n_max], with sel_cnt [B][H_kv]")
-    dev = _device_of(c)
-    return (_tensor(sel_idx, torch.int32, dev, 0, "sel_idx"), _tensor(sel_cnt, torch.int32, dev, c.B * c.H_kv, "sel_cnt"),
-            int(sel_idx.shape[2]))
+    return (_tensor(sel_idx, torch.int32, device, 0, "sel_idx"),
+            _tensor(sel_cnt, torch.int32, device, st.B * st.H_kv, "sel_cnt"), shape[2])
 
 
 def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_params:
@@ -526,21 +529,21 @@ def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_p
 
 def sba_append_kv4(c: Cache4, k_new: torch.Tensor, v_new: torch.Tensor, pos_start: torch.Tensor, stream=None):
     """k_new, v_new: bf16 [B][n_new][H_kv][d] to positions pos_start[s] .. of a four-bit cache."""
-    st, dev = c.struct(), c.kv.device
-    n_new = int(k_new.shape[1])
-    rows = c.B * n_new * c.H_kv * c.d
-    _check(load().sba_append_kv4(ctypes.byref(st), _tensor(k_new, torch.bfloat16, dev, rows, "k_new"),
+    ref, st, dev = _opened(c)
+    n_new = k_new.shape[1]
+    rows = st.B * n_new * st.H_kv * st.d
+    _check(load().sba_append_kv4(ref, _tensor(k_new, torch.bfloat16, dev, rows, "k_new"),
                                  _tensor(v_new, torch.bfloat16, dev, rows, "v_new"),
-                                 _tensor(pos_start, torch.int32, dev, c.B, "pos_start"), n_new,
+                                 _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n_new,
                                  _current(dev, stream)), "sba_append_kv4")
 
 
 def sba_read_kv4(c: Cache4, pos_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
     """Positions pos_start[s] .. as bf16 rows k_out, v_out [B][n][H_kv][d]."""
-    st, dev = c.struct(), c.kv.device
-    n = int(k_out.shape[1])
-    rows = c.B * n * c.H_kv * c.d
-    _check(load().sba_read_kv4(ctypes.byref(st), _tensor(pos_start, torch.int32, dev, c.B, "pos_start"), n,
+    ref, st, dev = _opened(c)
+    n = k_out.shape[1]
+    rows = st.B * n * st.H_kv * st.d
+    _check(load().sba_read_kv4(ref, _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n,
                                _tensor(k_out, torch.bfloat16, dev, rows, "k_out"),
                                _tensor(v_out, torch.bfloat16, dev, rows, "v_out"), _current(dev, stream)),
            "sba_read_kv4")
@@ -553,11 +556,11 @@ def sba_score_select_kv4_workspace_size(c: Cache4, p: sba_select_params) -> int:
 def sba_score_select_kv4(c: Cache4, q: torch.Tensor, p: sba_select_params, sel_idx: torch.Tensor,
                          sel_cnt: torch.Tensor, ws: torch.Tensor, stream=None):
     """q: bf16 [B][H_q][d] or [B][M][H_q][d]; one Quest selection per (sequence, group)."""
-    st, (qp, M) = c.struct(), _rows_of(c, q)
-    si, sc, n_max = _selection(c, sel_idx, sel_cnt)
-    _check(load().sba_score_select_kv4(ctypes.byref(st), qp, M, ctypes.byref(p), si, sc, n_max,
-                                       _tensor(ws, torch.uint8, c.kv.device, 0, "ws"), ws.numel(),
-                                       _current(c.kv.device, stream)), "sba_score_select_kv4")
+    ref, st, dev = _opened(c)
+    qp, M = _rows_of(st, dev, q)
+    si, sc, n_max = _selection(st, dev, sel_idx, sel_cnt)
+    _check(load().sba_score_select_kv4(ref, qp, M, ctypes.byref(p), si, sc, n_max, _tensor(ws, torch.uint8, dev, 0, "ws"),
+                                       ws.numel(), _current(dev, stream)), "sba_score_select_kv4")
 
 
 def sba_decode_kv4_workspace_size(c: Cache4, M: int = 1, n_max: int = 0) -> int:
@@ -570,26 +573,25 @@ def sba_decode_kv4(c: Cache4, q: torch.Tensor, softmax_scale: float, out: torch.
     """Attention over the selected blocks (or all) of a four-bit cache.  q, out: [B][H_q][d] or
     [B][M][H_q][d]; lse_out fp32 [B][M][H_q]; ws: uint8, zeroed once, of
     sba_decode_kv4_workspace_size(c, M, n_max) bytes."""
-    st, dev = c.struct(), c.kv.device
-    qp, M = _rows_of(c, q)
-    si, sc, n_max = _selection(c, sel_idx, sel_cnt)
-    if out.dtype not in (torch.bfloat16, torch.float32):
+    ref, st, dev = _opened(c)
+    qp, M = _rows_of(st, dev, q)
+    si, sc, n_max = _selection(st, dev, sel_idx, sel_cnt)
+    dt = out.dtype
+    if dt is not torch.bfloat16 and dt is not torch.float32:
         raise ValueError("out must be fp32 or bf16")
-    rows = c.B * M * c.H_q
-    _check(load().sba_decode_kv4(ctypes.byref(st), qp, M, si, sc, n_max, softmax_scale,
-                                 _tensor(out, out.dtype, dev, rows * c.d, "out"),
-                                 SBA_OUT_BF16 if out.dtype == torch.bfloat16 else SBA_OUT_F32,
+    rows = st.B * M * st.H_q
+    _check(load().sba_decode_kv4(ref, qp, M, si, sc, n_max, softmax_scale, _tensor(out, dt, dev, rows * st.d, "out"),
+                                 SBA_OUT_BF16 if dt is torch.bfloat16 else SBA_OUT_F32,
                                  _tensor(lse_out, torch.float32, dev, rows, "lse_out"),
                                  _tensor(ws, torch.uint8, dev, 0, "ws"), ws.numel(), _current(dev, stream)),
            "sba_decode_kv4")
 
 
-def _weights_args(c, q, lse, acc_in, acc_out, sel_idx, sel_cnt):
-    dev = _device_of(c)
-    qp, M = _rows_of(c, q)
-    si, sc, n_max = _selection(c, sel_idx, sel_cnt)
-    cells = c.num_pages * c.H_kv * c.b
-    return (qp, M, si, sc, n_max, _tensor(lse, torch.float32, dev, c.B * M * c.H_q, "lse"),
+def _weights_args(st, dev, q, lse, acc_in, acc_out, sel_idx, sel_cnt):
+    qp, M = _rows_of(st, dev, q)
+    si, sc, n_max = _selection(st, dev, sel_idx, sel_cnt)
+    cells = st.num_pages * st.H_kv * st.b
+    return (qp, M, si, sc, n_max, _tensor(lse, torch.float32, dev, st.B * M * st.H_q, "lse"),
             _tensor(acc_in, torch.float32, dev, cells, "acc_in"), _tensor(acc_out, torch.float32, dev, cells, "acc_out"))
 
 
@@ -599,32 +601,31 @@ def sba_accumulate_weights(c: Cache, q: torch.Tensor, lse: torch.Tensor, softmax
                            stream=None):
     """acc_out[t] = acc_in[t] + the attention weight token t received from q's rows (fp32
     [num_pages][H_kv][b]; acc_out may be acc_in); lse as the step's attention returned it."""
-    st = c.struct()
-    qp, M, si, sc, n_max, lp, ai, ao = _weights_args(c, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
-    gb = _tensor(gate_bias, torch.float32, c.k.device, c.B * c.H_q * n_max, "gate_bias")
-    _check(load().sba_accumulate_weights(ctypes.byref(st), qp, M, si, sc, gb, n_max, softmax_scale, lp, ai, ao,
-                                         _current(c.k.device, stream)), "sba_accumulate_weights")
+    ref, st, dev = _opened(c)
+    qp, M, si, sc, n_max, lp, ai, ao = _weights_args(st, dev, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
+    gb = _tensor(gate_bias, torch.float32, dev, st.B * st.H_q * n_max, "gate_bias")
+    _check(load().sba_accumulate_weights(ref, qp, M, si, sc, gb, n_max, softmax_scale, lp, ai, ao,
+                                         _current(dev, stream)), "sba_accumulate_weights")
 
 
 def sba_accumulate_weights_kv4(c: Cache4, q: torch.Tensor, lse: torch.Tensor, softmax_scale: float,
                                acc_in: torch.Tensor, acc_out: torch.Tensor, sel_idx: Optional[torch.Tensor] = None,
                                sel_cnt: Optional[torch.Tensor] = None, stream=None):
     """sba_accumulate_weights on a four-bit cache."""
-    st = c.struct()
-    qp, M, si, sc, n_max, lp, ai, ao = _weights_args(c, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
-    _check(load().sba_accumulate_weights_kv4(ctypes.byref(st), qp, M, si, sc, n_max, softmax_scale, lp, ai, ao,
-                                             _current(c.kv.device, stream)), "sba_accumulate_weights_kv4")
+    ref, st, dev = _opened(c)
+    qp, M, si, sc, n_max, lp, ai, ao = _weights_args(st, dev, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
+    _check(load().sba_accumulate_weights_kv4(ref, qp, M, si, sc, n_max, softmax_scale, lp, ai, ao,
+                                             _current(dev, stream)), "sba_accumulate_weights_kv4")
 
 
 def _evict(call, name, src, acc, p, dst, new_lens, kept, acc_dst, stream):
-    ss, ds, dev = src.struct(), dst.struct(), _device_of(src)
-    if _device_of(dst) != dev:
+    (sref, ss, dev), (dref, ds, dst_dev) = _opened(src), _opened(dst)
+    if dst_dev != dev:
         raise ValueError("source and destination caches are on different devices")
-    _check(call(ctypes.byref(ss), _tensor(acc, torch.float32, dev, src.num_pages * src.H_kv * src.b, "acc"),
-                ctypes.byref(p), ctypes.byref(ds),
-                _tensor(acc_dst, torch.float32, dev, dst.num_pages * dst.H_kv * dst.b, "acc_dst"),
-                _tensor(new_lens, torch.int32, dev, src.B, "new_lens"),
-                _tensor(kept, torch.int32, dev, src.B * src.H_kv * p.n_keep, "kept"), _current(dev, stream)), name)
+    _check(call(sref, _tensor(acc, torch.float32, dev, ss.num_pages * ss.H_kv * ss.b, "acc"), ctypes.byref(p), dref,
+                _tensor(acc_dst, torch.float32, dev, ds.num_pages * ds.H_kv * ds.b, "acc_dst"),
+                _tensor(new_lens, torch.int32, dev, ss.B, "new_lens"),
+                _tensor(kept, torch.int32, dev, ss.B * ss.H_kv * p.n_keep, "kept"), _current(dev, stream)), name)
 
 
 def sba_evict(src: Cache, acc: torch.Tensor, p: sba_evict_params, dst: Cache, new_lens: torch.Tensor,

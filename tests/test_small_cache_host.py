@@ -208,20 +208,35 @@ def test_bad_evict():
     assert lib.sba_evict(c16(), 0x5000, None, c16(**other), None, 0x6000, 0x7000, None) == ARG
 
 
-def test_binding_takes_device_tensors_of_the_right_kind_only():
+def test_binding_takes_device_tensors_of_the_right_kind_only(monkeypatch):
     kv = torch.zeros((4, 2, 2, 4608), dtype=torch.uint8)
     lens = torch.zeros(1, dtype=torch.int32)
     good = dict(kv=kv, seq_lens=lens, H_q=4, max_blocks=4, max_len=256)
     rows = torch.zeros((1, 1, 2, 128), dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="device"):
+    with pytest.raises(ValueError, match="device tensors"):
         sba.sba_append_kv4(sba.Cache4(**good), rows, rows, lens)
     with pytest.raises(ValueError, match="kv must be"):
         sba.Cache4(**{**good, "kv": kv[..., :4600].contiguous()}).struct()
-    with pytest.raises(ValueError, match="kv must be"):
-        sba.Cache4(**{**good, "kv": kv.to(torch.int8)}).struct()
-    with pytest.raises(ValueError, match="seq_lens"):
-        sba.Cache4(**{**good, "seq_lens": lens.long()}).struct()
-    with pytest.raises(ValueError, match="block_table"):
-        sba.Cache4(**good, block_table=torch.zeros((1, 3), dtype=torch.int32)).struct()
-    with pytest.raises(ValueError, match="desc"):
-        sba.Cache4(**good, desc=torch.zeros((4, 2, 2, 64), dtype=torch.bfloat16)).struct()
+    # what each argument has to be (device -1 is the CPU's)
+    for t, why in ((torch.zeros(4), "int32"), (torch.zeros(3, dtype=torch.int32), "at least 4"),
+                   (torch.zeros((4, 2), dtype=torch.int32).t(), "not contiguous")):
+        with pytest.raises(ValueError, match=why):
+            sba._tensor(t, torch.int32, -1, 4, "x")
+    with pytest.raises(ValueError, match="cuda:3"):
+        sba._tensor(torch.zeros(4, dtype=torch.int32), torch.int32, 3, 4, "x")
+    assert sba._tensor(None, torch.int32, 0, 4, "x") is None
+    st = sba.sba_cache4(B=2, H_q=8, H_kv=2, d=128)
+    assert sba._rows_of(st, -1, torch.zeros((2, 3, 8, 128), dtype=torch.bfloat16))[1] == 3
+    assert sba._rows_of(st, -1, torch.zeros((2, 8, 128), dtype=torch.bfloat16))[1] == 1
+    for shape in ((2, 8, 64), (1, 8, 128), (2, 3, 4, 128), (16, 128)):
+        with pytest.raises(ValueError, match="q must be"):
+            sba._rows_of(st, -1, torch.zeros(shape, dtype=torch.bfloat16))
+    idx, cnt = torch.zeros((2, 2, 5), dtype=torch.int32), torch.zeros((2, 2), dtype=torch.int32)
+    assert sba._selection(st, -1, idx, cnt)[2] == 5 and sba._selection(st, -1, None, None) == (None, None, 0)
+    for i, c in ((idx, None), (None, cnt), (idx[0], cnt), (idx.long(), cnt), (idx, cnt[:1])):
+        with pytest.raises(ValueError):
+            sba._selection(st, -1, i, c)
+    # kernels run on the current device: tensors of another one are refused
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        sba._current(0, None)
