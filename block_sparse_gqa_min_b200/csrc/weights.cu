@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.cuh"
+#include "tc.cuh"
 
 namespace sba {
 
@@ -274,6 +275,224 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many query rows: the products on tcgen05.  A tile of 128 tokens is the MMA's M, 64 query rows its N:
+// a warp brings its strip of 32 tokens from codes to f16 and stores it as the A operand in tensor
+// memory, one thread issues the eight steps of 16 channels against the rows in shared memory, and every
+// thread reads back the 64 logits of ONE token, so the sum over the rows is in its own registers (no
+// shuffle, no shared memory).  What bounds it is the 16 exponentials a cycle of an SM.
+// Two warpgroups a CTA and two CTAs an SM work on tiles of their own: one's conversion and its wait for
+// the tensor core overlap the others' exponentials.
+// ---------------------------------------------------------------------------
+constexpr int kTcLeastRows = 24;
+constexpr int kTcThreads = 256;
+constexpr int kTcGroups = kTcThreads / 128;
+constexpr int kTcChunk = 64;                     // rows of one MMA
+constexpr int kTcRows = 256;                     // rows staged at a time
+constexpr int kTcSmem = 2 * kTcRows * 128 + 1024;
+constexpr uint32_t kTcGroupCols = 128;           // A: 64 columns (f16 pairs), D: 64 (fp32)
+constexpr uint32_t kTcCols = kTcGroups * kTcGroupCols;
+
+__global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Args a) {
+    extern __shared__ uint8_t dyn_raw[];
+    uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ float2 row_p[kTcRows];  // scale, lse (both in log2 units)
+    __shared__ int row_lim[kTcRows];
+    __shared__ int chunk_plain[kTcRows / kTcChunk];  // every real row of the chunk has an lse
+    __shared__ uint64_t done[kTcGroups];
+    __shared__ uint32_t tmem_at;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = tid >> 7;
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int G = a.H_q / a.H_kv;
+    if (tid == 0) {
+        for (int i = 0; i < kTcGroups; ++i) mbar_init(&done[i], 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) tc::alloc(&tmem_at, kTcCols);
+    pdl_wait();
+    pdl_trigger();
+
+    const int len = max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b));
+    const int N = blocks_of(len, a.b);
+    int nb = N;
+    const int32_t* sel = nullptr;
+    if (a.sel_idx) {
+        nb = __ldca(a.sel_cnt + s * a.H_kv + h);
+        if (nb < 0 || nb > a.n_max) {
+            if (tid == 0 && blockIdx.x == 0) report(a.status, SBA_DEV_BAD_SELECTION);
+            nb = nb < 0 ? 0 : a.n_max;
+        }
+        sel = a.sel_idx + ((int64_t)s * a.H_kv + h) * a.n_max;
+    }
+    // tiles of four strips; this warp's strip of tile t is 4t + warp % 4
+    const int spb = a.b / kStripTokens;
+    const int64_t T = ((int64_t)nb * spb + 3) / 4;
+    const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
+    const int mine = t0 + group < t1 ? (t1 - t0 - group + kTcGroups - 1) / kTcGroups : 0;
+
+    int64_t row = -1;
+    int tok = 0;
+    auto resolve = [&](int x) {  // lane x: this warp's strip of the group's tile 32 * batch + x
+        row = -1;
+        tok = 0;
+        if (x >= mine) return;
+        const int g = 4 * (t0 + group + kTcGroups * x) + (warp & 3), pos = g / spb;
+        if (pos >= nb) return;
+        const int j = sel ? __ldca(sel + pos) : pos;
+        if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
+            report(a.status, SBA_DEV_BAD_SELECTION);
+            return;
+        }
+        const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
+        tok = j * a.b + (g % spb) * kStripTokens;
+        if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % spb) * kStripTokens;
+    };
+
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tm = tmem_at + group * kTcGroupCols;
+    const uint32_t my_lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int first_hidden = len - a.M + 1;
+    uint32_t phase = 0;
+    bool alive = true;
+
+    for (int r0 = 0; r0 < a.rows && t0 < t1; r0 += kTcRows) {
+        const int n_rows = min(kTcRows, a.rows - r0), n_pad = (n_rows + 15) & ~15;
+        if (r0) __syncthreads();
+        if (tid < kTcRows / kTcChunk) chunk_plain[tid] = 1;
+        __syncthreads();
+        // ---- the rows, scaled to a maximum in [1, 2) each, as f16 in the B operand's layout: 16 lanes a
+        // row, lane m the 16-byte chunk m of its 128 positions (64 in each half).  Position 16p + 4i + x
+        // is channel 32i + 4p + x, the order in which the key operand is stored ----
+        for (int r = tid >> 4; r < n_pad; r += kTcThreads / 16) {
+            const int m = tid & 15, p = m >> 1, i0 = 2 * (m & 1), gr = r0 + r;
+            uint2 x0 = make_uint2(0u, 0u), x1 = x0;
+            int64_t qrow = 0;
+            if (r < n_rows) {
+                qrow = ((int64_t)s * a.M + gr / G) * a.H_q + h * G + gr % G;
+                const uint2* src = reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim);
+                x0 = __ldca(src + 8 * i0 + p);
+                x1 = __ldca(src + 8 * (i0 + 1) + p);
+            }
+            const uint32_t w[4] = {x0.x, x0.y, x1.x, x1.y};
+            float mx = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            const int e2 = row_exponent(mx);
+            const float down = pow2(-e2);
+            uint32_t f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+            *reinterpret_cast<uint4*>(qs + (m >> 3) * (kTcRows * 128) + r * 128 + (((m & 7) ^ (r & 7)) << 4)) =
+                make_uint4(f[0], f[1], f[2], f[3]);
+            if (m == 0) {
+                const float lse = r < n_rows ? __ldca(a.lse + qrow) : -INFINITY;
+                const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
+                row_p[r] = counts ? make_float2(a.scale_log2 * pow2(e2), lse * kLog2e) : make_float2(0.f, INFINITY);
+                row_lim[r] = counts ? len - a.M + gr / G + 1 : 0;
+                if (!counts && r < n_rows) chunk_plain[r / kTcChunk] = 0;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncthreads();
+
+        const float* acc_from = r0 ? a.acc_out : a.acc_in;
+        const uint64_t db = tc::smem_desc(smem_u32(qs), 1024);
+        Keys<true> next[2];
+        auto fetch = [&](int x) {
+            if ((x & 31) == 0) resolve(x + lane);
+            const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
+            if (from >= 0) {
+                next[0].load(a.k, from, lane);
+                next[1].load(a.k, from + 16, lane);
+            }
+        };
+        if (mine > 0) fetch(0);
+        for (int x = 0; x < mine; ++x) {
+            const int64_t cur_row = __shfl_sync(0xffffffffu, row, x & 31);
+            const int cur_tok = __shfl_sync(0xffffffffu, tok, x & 31) + lane;
+            const bool real = cur_row >= 0 && cur_tok < len;
+            // ---- keys to the A operand (a strip that is not there leaves what it held: its tokens are not written) ----
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t f[8][4], v[32];
+                next[half].operand(f);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {  // columns 8ks + 2i, + 1 of rows tr and tr + 8
+                    v[4 * ks] = f[ks][0];
+                    v[4 * ks + 1] = f[ks][2];
+                    v[4 * ks + 2] = f[ks][1];
+                    v[4 * ks + 3] = f[ks][3];
+                }
+                tc::st_16x256b_x8(tm + my_lanes + ((uint32_t)(16 * half) << 16), v);
+            }
+            const float before = real ? acc_from[cur_row + lane] : 0.f;
+            if (x + 1 < mine) fetch(x + 1);
+            tc::wait_st();
+            float w = 0.f;
+            for (int c0 = 0; c0 < n_rows; c0 += kTcChunk) {
+                const int n = min(kTcChunk, n_pad - c0);
+                // every thread has stored its keys and read its logits of the chunk before
+                tc::fence_before();
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                if ((tid & 127) == 0 && alive) {
+                    tc::fence_after();
+                    const uint32_t id = tc::idesc(128, n, false);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_ts(tm + 64, tm + 8 * kk,
+                                   db + (uint64_t)(((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32 + c0 * 128) >> 4), id, kk > 0);
+                    tc::commit(&done[group]);
+                }
+                // a wait that ran out leaves the thread to the barriers only
+                if (alive) alive = mbar_wait(&done[group], phase, a.status);
+                phase ^= 1;
+                tc::fence_after();
+                const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, cur_tok < first_hidden);
+                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int b = 0; b < kTcChunk; b += 16) {
+                    if (b >= n) break;
+                    uint32_t d[16];
+                    tc::ld16(tm + 64 + my_lanes + b, d);
+                    tc::wait_ld();
+                    const float4* rp = reinterpret_cast<const float4*>(row_p + c0 + b);
+                    if (all_seen) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 q = rp[e >> 1];
+                            sum[0] += ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
+                            sum[1] += ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float4 q = rp[e >> 1];
+                            const float p0 = ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
+                            const float p1 = ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
+                            sum[0] += cur_tok < row_lim[c0 + b + e] ? p0 : 0.f;
+                            sum[1] += cur_tok < row_lim[c0 + b + e + 1] ? p1 : 0.f;
+                        }
+                    }
+                }
+                w += sum[0] + sum[1];
+            }
+            if (real && alive) a.acc_out[cur_row + lane] = before + w;
+        }
+    }
+    if (!alive && (tid & 127) == 0) mbar_wait(&done[group], phase ^ 1, a.status);  // products still in flight
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::fence_after();
+        tc::dealloc(tmem_at, kTcCols);
+    }
+}
+
 template <bool kFour, class Cache>
 int launch_weights(const Cache& c, const void* keys, const void* q, int M, const int32_t* sel_idx,
                    const int32_t* sel_cnt, const float* gate_bias, int n_max, float scale, const float* lse,
@@ -299,6 +518,14 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     a.lse = lse;
     a.acc_in = acc_in;
     a.acc_out = acc_out;
+    if (kFour && a.rows >= kTcLeastRows) {
+        if (allow_smem<accumulate_weights_tc_kernel>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
+        const int64_t tiles = ((int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kStripTokens) + 3) / 4;
+        const int64_t most = (tiles + kTcGroups - 1) / kTcGroups, want = 6 * 2 * 148 / ((int64_t)c.B * c.H_kv);
+        const int64_t x = want < 1 ? 1 : want;
+        dim3 grid((unsigned)(x < most ? x : most < 1 ? 1 : most), c.H_kv, c.B);
+        return launch(accumulate_weights_tc_kernel, grid, dim3(kTcThreads), kTcSmem, stream, a);
+    }
     // one tile a warp at least; up to eight CTAs per SM's worth of them, so ragged lengths even out
     const int64_t tiles = (int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kTileTokens);
     const int64_t most = (tiles + kWarps - 1) / kWarps, want = 8 * 148 / ((int64_t)c.B * c.H_kv);

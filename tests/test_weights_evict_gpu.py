@@ -68,6 +68,9 @@ WEIGHTS = [
     (False, 64, [4096, 100], 2, 5, True, 1, 16, True),
     (False, 128, [5000], 2, 16, False, 1, 7, True),
     (True, 64, [600], 1, 3, False, 5, 4, False),
+    (True, 64, [900, 5], 1, 16, True, 20, 0, False),     # 320 rows
+    (True, 64, [3000, 70], 2, 6, True, 4, 9, False),     # 24 rows over an odd number of blocks
+    (True, 128, [4000], 1, 11, False, 7, 5, False),      # 77 rows
 ]
 
 
