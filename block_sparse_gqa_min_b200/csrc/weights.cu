@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
 // memory, one thread issues the eight steps of 16 channels against the rows in shared memory, and every
 // thread reads back the 64 logits of ONE token, so the sum over the rows is in its own registers (no
 // shuffle, no shared memory).  What bounds it is the 16 exponentials a cycle of an SM.
-// Two warpgroups a CTA and two CTAs an SM work on tiles of their own: one's conversion and its wait for
-// the tensor core overlap the others' exponentials.
+// Two CTAs of two warpgroups share an SM; every warpgroup works on tiles of its own, so one's conversion
+// and its wait for the tensor core overlap the others' exponentials.
 // ---------------------------------------------------------------------------
 constexpr int kTcLeastRows = 24;
 constexpr int kTcThreads = 256;
@@ -352,8 +352,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = tmem_at + group * kTcGroupCols;
-    const uint32_t my_lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tm = tmem_at + group * kTcGroupCols, my_lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int first_hidden = len - a.M + 1;
     uint32_t phase = 0;
     bool alive = true;
@@ -363,38 +362,64 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
         if (r0) __syncthreads();
         if (tid < kTcRows / kTcChunk) chunk_plain[tid] = 1;
         __syncthreads();
+        Keys<true> next[2];
+        int64_t from = -1;  // cache row of the strip held in `next`, and its first token
+        int from_tok = 0;
+        auto fetch = [&](int x) {
+            if ((x & 31) == 0) resolve(x + lane);
+            from = __shfl_sync(0xffffffffu, row, x & 31);
+            from_tok = __shfl_sync(0xffffffffu, tok, x & 31);
+            if (from >= 0) {
+                next[0].load(a.k, from, lane);
+                next[1].load(a.k, from + 16, lane);
+            }
+        };
+        if (mine > 0) fetch(0);
         // ---- the rows, scaled to a maximum in [1, 2) each, as f16 in the B operand's layout: 16 lanes a
         // row, lane m the 16-byte chunk m of its 128 positions (64 in each half).  Position 16p + 4i + x
         // is channel 32i + 4p + x, the order in which the key operand is stored ----
-        for (int r = tid >> 4; r < n_pad; r += kTcThreads / 16) {
-            const int m = tid & 15, p = m >> 1, i0 = 2 * (m & 1), gr = r0 + r;
-            uint2 x0 = make_uint2(0u, 0u), x1 = x0;
-            int64_t qrow = 0;
-            if (r < n_rows) {
-                qrow = ((int64_t)s * a.M + gr / G) * a.H_q + h * G + gr % G;
-                const uint2* src = reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim);
-                x0 = __ldca(src + 8 * i0 + p);
-                x1 = __ldca(src + 8 * (i0 + 1) + p);
+        constexpr int kStep = kTcThreads / 16, kBatch = 4;  // rows of one pass, passes whose loads go together
+        const int m = tid & 15, p = m >> 1, i0 = 2 * (m & 1);
+        for (int rb = tid >> 4; rb < n_pad; rb += kStep * kBatch) {
+            uint2 x0[kBatch], x1[kBatch];
+            float lse[kBatch];
+#pragma unroll
+            for (int y = 0; y < kBatch; ++y) {
+                const int r = rb + y * kStep, gr = r0 + r;
+                x0[y] = x1[y] = make_uint2(0u, 0u);
+                lse[y] = -INFINITY;
+                if (r < n_rows) {
+                    const int64_t qrow = ((int64_t)s * a.M + gr / G) * a.H_q + h * G + gr % G;
+                    const uint2* src = reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim);
+                    x0[y] = __ldca(src + 8 * i0 + p);
+                    x1[y] = __ldca(src + 8 * (i0 + 1) + p);
+                    lse[y] = __ldca(a.lse + qrow);
+                }
             }
-            const uint32_t w[4] = {x0.x, x0.y, x1.x, x1.y};
-            float mx = 0.f;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+            for (int y = 0; y < kBatch; ++y) {
+                const int r = rb + y * kStep;
+                if (r >= n_pad) break;  // the same for a whole warp: n_pad is a multiple of 16
+                const uint32_t w[4] = {x0[y].x, x0[y].y, x1[y].x, x1[y].y};
+                float mx = 0.f;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e2 = row_exponent(mx);
-            const float down = pow2(-e2);
-            uint32_t f[4];
+                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
-            *reinterpret_cast<uint4*>(qs + (m >> 3) * (kTcRows * 128) + r * 128 + (((m & 7) ^ (r & 7)) << 4)) =
-                make_uint4(f[0], f[1], f[2], f[3]);
-            if (m == 0) {
-                const float lse = r < n_rows ? __ldca(a.lse + qrow) : -INFINITY;
-                const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
-                row_p[r] = counts ? make_float2(a.scale_log2 * pow2(e2), lse * kLog2e) : make_float2(0.f, INFINITY);
-                row_lim[r] = counts ? len - a.M + gr / G + 1 : 0;
-                if (!counts && r < n_rows) chunk_plain[r / kTcChunk] = 0;
+                for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const int e2 = row_exponent(mx);
+                const float down = pow2(-e2);
+                uint32_t f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+                *reinterpret_cast<uint4*>(qs + (m >> 3) * (kTcRows * 128) + r * 128 + (((m & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(f[0], f[1], f[2], f[3]);
+                if (m == 0) {
+                    // a row that attended to nothing adds nothing
+                    const bool counts = lse[y] > -INFINITY || lse[y] != lse[y];
+                    row_p[r] = counts ? make_float2(a.scale_log2 * pow2(e2), lse[y] * kLog2e) : make_float2(0.f, INFINITY);
+                    row_lim[r] = counts ? len - a.M + (r0 + r) / G + 1 : 0;
+                    if (!counts && r < n_rows) chunk_plain[r / kTcChunk] = 0;
+                }
             }
         }
         fence_proxy_async_smem();
@@ -402,21 +427,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
 
         const float* acc_from = r0 ? a.acc_out : a.acc_in;
         const uint64_t db = tc::smem_desc(smem_u32(qs), 1024);
-        Keys<true> next[2];
-        auto fetch = [&](int x) {
-            if ((x & 31) == 0) resolve(x + lane);
-            const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
-            if (from >= 0) {
-                next[0].load(a.k, from, lane);
-                next[1].load(a.k, from + 16, lane);
-            }
-        };
-        if (mine > 0) fetch(0);
         for (int x = 0; x < mine; ++x) {
-            const int64_t cur_row = __shfl_sync(0xffffffffu, row, x & 31);
-            const int cur_tok = __shfl_sync(0xffffffffu, tok, x & 31) + lane;
-            const bool real = cur_row >= 0 && cur_tok < len;
-            // ---- keys to the A operand (a strip that is not there leaves what it held: its tokens are not written) ----
+            // ---- keys of `next` to the A operand (a strip that is not there leaves what `next` held: its
+            // tokens are not written) ----
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t f[8][4], v[32];
@@ -430,13 +443,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                 }
                 tc::st_16x256b_x8(tm + my_lanes + ((uint32_t)(16 * half) << 16), v);
             }
-            const float before = real ? acc_from[cur_row + lane] : 0.f;
+            const int64_t this_row = from + lane;
+            const int this_tok = from_tok + lane;
+            const bool real = from >= 0 && this_tok < len;
+            const float before = real ? acc_from[this_row] : 0.f;
             if (x + 1 < mine) fetch(x + 1);
             tc::wait_st();
             float w = 0.f;
             for (int c0 = 0; c0 < n_rows; c0 += kTcChunk) {
                 const int n = min(kTcChunk, n_pad - c0);
-                // every thread has stored its keys and read its logits of the chunk before
+                // every thread of the group has stored its keys and read its logits of the chunk before
                 tc::fence_before();
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                 if ((tid & 127) == 0 && alive) {
@@ -452,8 +468,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                 if (alive) alive = mbar_wait(&done[group], phase, a.status);
                 phase ^= 1;
                 tc::fence_after();
-                const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, cur_tok < first_hidden);
-                float sum[2] = {0.f, 0.f};
+                const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, this_tok < first_hidden);
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int b = 0; b < kTcChunk; b += 16) {
                     if (b >= n) break;
@@ -465,8 +481,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
 #pragma unroll
                         for (int e = 0; e < 16; e += 2) {
                             const float4 q = rp[e >> 1];
-                            sum[0] += ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
-                            sum[1] += ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
+                            sum.x += ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
+                            sum.y += ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
                         }
                     } else {
 #pragma unroll
@@ -474,14 +490,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                             const float4 q = rp[e >> 1];
                             const float p0 = ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
                             const float p1 = ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
-                            sum[0] += cur_tok < row_lim[c0 + b + e] ? p0 : 0.f;
-                            sum[1] += cur_tok < row_lim[c0 + b + e + 1] ? p1 : 0.f;
+                            sum.x += this_tok < row_lim[c0 + b + e] ? p0 : 0.f;
+                            sum.y += this_tok < row_lim[c0 + b + e + 1] ? p1 : 0.f;
                         }
                     }
                 }
-                w += sum[0] + sum[1];
+                w += sum.x + sum.y;
             }
-            if (real && alive) a.acc_out[cur_row + lane] = before + w;
+            if (real && alive) a.acc_out[this_row] = before + w;
         }
     }
     if (!alive && (tid & 127) == 0) mbar_wait(&done[group], phase ^ 1, a.status);  // products still in flight
@@ -521,7 +537,7 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     if (kFour && a.rows >= kTcLeastRows) {
         if (allow_smem<accumulate_weights_tc_kernel>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
         const int64_t tiles = ((int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kStripTokens) + 3) / 4;
-        const int64_t most = (tiles + kTcGroups - 1) / kTcGroups, want = 6 * 2 * 148 / ((int64_t)c.B * c.H_kv);
+        const int64_t most = (tiles + kTcGroups - 1) / kTcGroups, want = 4 * 2 * 148 / ((int64_t)c.B * c.H_kv);
         const int64_t x = want < 1 ? 1 : want;
         dim3 grid((unsigned)(x < most ? x : most < 1 ? 1 : most), c.H_kv, c.B);
         return launch(accumulate_weights_tc_kernel, grid, dim3(kTcThreads), kTcSmem, stream, a);
