@@ -13,6 +13,8 @@
 // With few rows the bytes of K bound it (one read of 256 or 72 bytes a token); with many, the MMAs.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.cuh"
@@ -33,7 +35,7 @@ struct Args {
     const int32_t* block_table;
     const int32_t* seq_lens;
     int32_t* status;
-    int H_q, H_kv, b, max_blocks, num_pages, M, rows;
+    int B, H_q, H_kv, b, max_blocks, num_pages, M, rows;
     const __nv_bfloat16* q;
     const int32_t* sel_idx;
     const int32_t* sel_cnt;
@@ -293,18 +295,35 @@ constexpr int kTcSmem = 2 * kTcRows * 128 + 1024;
 constexpr uint32_t kTcGroupCols = 128;           // A: 64 columns (f16 pairs), D: 64 (fp32)
 constexpr uint32_t kTcCols = kTcGroups * kTcGroupCols;
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Args a) {
     extern __shared__ uint8_t dyn_raw[];
     uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ float2 row_p[kTcRows];  // scale, lse (both in log2 units)
+    __shared__ float4 row_p[kTcRows / 2];  // of rows 2r, 2r + 1: their scales, and minus their lse (log2 units)
     __shared__ int row_lim[kTcRows];
     __shared__ int chunk_plain[kTcRows / kTcChunk];  // every real row of the chunk has an lse
     __shared__ uint64_t done[kTcGroups];
     __shared__ uint32_t tmem_at;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = tid >> 7;
-    const int h = blockIdx.y, s = blockIdx.z;
-    const int G = a.H_q / a.H_kv;
+    const int G = a.H_q / a.H_kv, spb = a.b / kStripTokens;
     if (tid == 0) {
         for (int i = 0; i < kTcGroups; ++i) mbar_init(&done[i], 1);
         fence_mbar_init();
@@ -313,191 +332,226 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     pdl_wait();
     pdl_trigger();
 
-    const int len = max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b));
-    const int N = blocks_of(len, a.b);
-    int nb = N;
-    const int32_t* sel = nullptr;
-    if (a.sel_idx) {
-        nb = __ldca(a.sel_cnt + s * a.H_kv + h);
-        if (nb < 0 || nb > a.n_max) {
-            if (tid == 0 && blockIdx.x == 0) report(a.status, SBA_DEV_BAD_SELECTION);
-            nb = nb < 0 ? 0 : a.n_max;
-        }
-        sel = a.sel_idx + ((int64_t)s * a.H_kv + h) * a.n_max;
-    }
-    // tiles of four strips; this warp's strip of tile t is 4t + warp % 4
-    const int spb = a.b / kStripTokens;
-    const int64_t T = ((int64_t)nb * spb + 3) / 4;
-    const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
-    const int mine = t0 + group < t1 ? (t1 - t0 - group + kTcGroups - 1) / kTcGroups : 0;
-
-    int64_t row = -1;
-    int tok = 0;
-    auto resolve = [&](int x) {  // lane x: this warp's strip of the group's tile 32 * batch + x
-        row = -1;
-        tok = 0;
-        if (x >= mine) return;
-        const int g = 4 * (t0 + group + kTcGroups * x) + (warp & 3), pos = g / spb;
-        if (pos >= nb) return;
-        const int j = sel ? __ldca(sel + pos) : pos;
-        if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
-            report(a.status, SBA_DEV_BAD_SELECTION);
-            return;
-        }
-        const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
-        tok = j * a.b + (g % spb) * kStripTokens;
-        if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % spb) * kStripTokens;
+    // ---- this CTA's share: an equal part of all the units' tiles, whatever their lengths.  A tile is four
+    // strips, a unit one (sequence, KV head) ----
+    const int units = a.B * a.H_kv;
+    auto length = [&](int s) { return max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b)); };
+    auto blocks = [&](int u) {
+        if (!a.sel_idx) return blocks_of(length(u / a.H_kv), a.b);
+        const int n = __ldca(a.sel_cnt + u);
+        if (n < 0 || n > a.n_max) report(a.status, SBA_DEV_BAD_SELECTION);
+        return n < 0 ? 0 : min(n, a.n_max);
     };
+    auto tiles = [&](int u) { return u < units ? (blocks(u) * spb + 3) / 4 : 0; };
+    int64_t all = 0;
+    for (int u = lane; u < units; u += 32) all += tiles(u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    int64_t at = all * blockIdx.x / gridDim.x;  // first tile of the share, then within its unit
+    int left = (int)(all * (blockIdx.x + 1) / gridDim.x - at);
+    int unit = 0;
+    for (;; unit += 32) {
+        const int mine = tiles(unit + lane);
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, at < upto);
+        if (past || left == 0) {
+            const int x = past ? __ffs(past) - 1 : 0;
+            unit += x;
+            at -= __shfl_sync(0xffffffffu, upto - mine, x);
+            break;
+        }
+        at -= __shfl_sync(0xffffffffu, upto, 31);
+    }
 
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tm = tmem_at + group * kTcGroupCols, my_lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const int first_hidden = len - a.M + 1;
     uint32_t phase = 0;
     bool alive = true;
 
-    for (int r0 = 0; r0 < a.rows && t0 < t1; r0 += kTcRows) {
-        const int n_rows = min(kTcRows, a.rows - r0), n_pad = (n_rows + 15) & ~15;
-        if (r0) __syncthreads();
-        if (tid < kTcRows / kTcChunk) chunk_plain[tid] = 1;
-        __syncthreads();
-        Keys<true> next[2];
-        int64_t from = -1;  // cache row of the strip held in `next`, and its first token
-        int from_tok = 0;
-        auto fetch = [&](int x) {
-            if ((x & 31) == 0) resolve(x + lane);
-            from = __shfl_sync(0xffffffffu, row, x & 31);
-            from_tok = __shfl_sync(0xffffffffu, tok, x & 31);
-            if (from >= 0) {
-                next[0].load(a.k, from, lane);
-                next[1].load(a.k, from + 16, lane);
-            }
-        };
-        if (mine > 0) fetch(0);
-        // ---- the rows, scaled to a maximum in [1, 2) each, as f16 in the B operand's layout: 16 lanes a
-        // row, lane m the 16-byte chunk m of its 128 positions (64 in each half).  Position 16p + 4i + x
-        // is channel 32i + 4p + x, the order in which the key operand is stored ----
-        constexpr int kStep = kTcThreads / 16, kBatch = 4;  // rows of one pass, passes whose loads go together
-        const int m = tid & 15, p = m >> 1, i0 = 2 * (m & 1);
-        for (int rb = tid >> 4; rb < n_pad; rb += kStep * kBatch) {
-            uint2 x0[kBatch], x1[kBatch];
-            float lse[kBatch];
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                const int r = rb + y * kStep, gr = r0 + r;
-                x0[y] = x1[y] = make_uint2(0u, 0u);
-                lse[y] = -INFINITY;
-                if (r < n_rows) {
-                    const int64_t qrow = ((int64_t)s * a.M + gr / G) * a.H_q + h * G + gr % G;
-                    const uint2* src = reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim);
-                    x0[y] = __ldca(src + 8 * i0 + p);
-                    x1[y] = __ldca(src + 8 * (i0 + 1) + p);
-                    lse[y] = __ldca(a.lse + qrow);
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < kBatch; ++y) {
-                const int r = rb + y * kStep;
-                if (r >= n_pad) break;  // the same for a whole warp: n_pad is a multiple of 16
-                const uint32_t w[4] = {x0[y].x, x0[y].y, x1[y].x, x1[y].y};
-                float mx = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
-#pragma unroll
-                for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const int e2 = row_exponent(mx);
-                const float down = pow2(-e2);
-                uint32_t f[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
-                *reinterpret_cast<uint4*>(qs + (m >> 3) * (kTcRows * 128) + r * 128 + (((m & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(f[0], f[1], f[2], f[3]);
-                if (m == 0) {
-                    // a row that attended to nothing adds nothing
-                    const bool counts = lse[y] > -INFINITY || lse[y] != lse[y];
-                    row_p[r] = counts ? make_float2(a.scale_log2 * pow2(e2), lse[y] * kLog2e) : make_float2(0.f, INFINITY);
-                    row_lim[r] = counts ? len - a.M + (r0 + r) / G + 1 : 0;
-                    if (!counts && r < n_rows) chunk_plain[r / kTcChunk] = 0;
-                }
-            }
-        }
-        fence_proxy_async_smem();
-        __syncthreads();
+    for (; left > 0; ++unit, at = 0) {
+        const int s = unit / a.H_kv, h = unit % a.H_kv;
+        const int len = length(s), N = blocks_of(len, a.b), nb = blocks(unit);
+        const int32_t* sel = a.sel_idx ? a.sel_idx + (int64_t)unit * a.n_max : nullptr;
+        const int t0 = (int)at, n_tiles = min(left, (nb * spb + 3) / 4 - t0);
+        left -= n_tiles;
+        const int mine = group < n_tiles ? (n_tiles - group + kTcGroups - 1) / kTcGroups : 0;
+        const int first_hidden = len - a.M + 1;
 
-        const float* acc_from = r0 ? a.acc_out : a.acc_in;
-        const uint64_t db = tc::smem_desc(smem_u32(qs), 1024);
-        for (int x = 0; x < mine; ++x) {
-            // ---- keys of `next` to the A operand (a strip that is not there leaves what `next` held: its
-            // tokens are not written) ----
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t f[8][4], v[32];
-                next[half].operand(f);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {  // columns 8ks + 2i, + 1 of rows tr and tr + 8
-                    v[4 * ks] = f[ks][0];
-                    v[4 * ks + 1] = f[ks][2];
-                    v[4 * ks + 2] = f[ks][1];
-                    v[4 * ks + 3] = f[ks][3];
-                }
-                tc::st_16x256b_x8(tm + my_lanes + ((uint32_t)(16 * half) << 16), v);
+        int64_t row = -1;
+        int tok = 0;
+        auto resolve = [&](int x) {  // lane x: this warp's strip of the group's tile 32 * batch + x
+            row = -1;
+            tok = 0;
+            if (x >= mine) return;
+            const int g = 4 * (t0 + group + kTcGroups * x) + (warp & 3), pos = g / spb;
+            if (pos >= nb) return;
+            const int j = sel ? __ldca(sel + pos) : pos;
+            if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
+                report(a.status, SBA_DEV_BAD_SELECTION);
+                return;
             }
-            const int64_t this_row = from + lane;
-            const int this_tok = from_tok + lane;
-            const bool real = from >= 0 && this_tok < len;
-            const float before = real ? acc_from[this_row] : 0.f;
-            if (x + 1 < mine) fetch(x + 1);
-            tc::wait_st();
-            float w = 0.f;
-            for (int c0 = 0; c0 < n_rows; c0 += kTcChunk) {
-                const int n = min(kTcChunk, n_pad - c0);
-                // every thread of the group has stored its keys and read its logits of the chunk before
-                tc::fence_before();
-                asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                if ((tid & 127) == 0 && alive) {
-                    tc::fence_after();
-                    const uint32_t id = tc::idesc(128, n, false);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_ts(tm + 64, tm + 8 * kk,
-                                   db + (uint64_t)(((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32 + c0 * 128) >> 4), id, kk > 0);
-                    tc::commit(&done[group]);
+            const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
+            tok = j * a.b + (g % spb) * kStripTokens;
+            if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % spb) * kStripTokens;
+        };
+
+        for (int r0 = 0; r0 < a.rows && n_tiles > 0; r0 += kTcRows) {
+            const int n_rows = min(kTcRows, a.rows - r0), n_pad = (n_rows + 15) & ~15;
+            __syncthreads();  // the rows before are done with
+            if (tid < kTcRows / kTcChunk) chunk_plain[tid] = 1;
+            __syncthreads();
+            Keys<true> next[2];
+            int64_t from = -1;  // cache row of the strip held in `next`, and its first token
+            int from_tok = 0;
+            auto fetch = [&](int x) {
+                if ((x & 31) == 0) resolve(x + lane);
+                from = __shfl_sync(0xffffffffu, row, x & 31);
+                from_tok = __shfl_sync(0xffffffffu, tok, x & 31);
+                if (from >= 0) {
+                    next[0].load(a.k, from, lane);
+                    next[1].load(a.k, from + 16, lane);
                 }
-                // a wait that ran out leaves the thread to the barriers only
-                if (alive) alive = mbar_wait(&done[group], phase, a.status);
-                phase ^= 1;
-                tc::fence_after();
-                const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, this_tok < first_hidden);
-                float2 sum = make_float2(0.f, 0.f);
+            };
+            if (mine > 0) fetch(0);
+            // ---- the rows, scaled to a maximum in [1, 2) each, as f16 in the B operand's layout: 16 lanes a
+            // row, lane m the 16-byte chunk m of its 128 positions (64 in each half).  Position 16p + 4i + x
+            // is channel 32i + 4p + x, the order in which the key operand is stored ----
+            constexpr int kStep = kTcThreads / 16, kBatch = 4;  // rows of one pass, passes whose loads go together
+            const int m = tid & 15, p = m >> 1, i0 = 2 * (m & 1);
+            for (int rb = tid >> 4; rb < n_pad; rb += kStep * kBatch) {
+                uint2 x0[kBatch], x1[kBatch];
+                float lse[kBatch];
 #pragma unroll
-                for (int b = 0; b < kTcChunk; b += 16) {
-                    if (b >= n) break;
-                    uint32_t d[16];
-                    tc::ld16(tm + 64 + my_lanes + b, d);
-                    tc::wait_ld();
-                    const float4* rp = reinterpret_cast<const float4*>(row_p + c0 + b);
-                    if (all_seen) {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float4 q = rp[e >> 1];
-                            sum.x += ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
-                            sum.y += ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float4 q = rp[e >> 1];
-                            const float p0 = ex2(fmaf(__uint_as_float(d[e]), q.x, -q.y));
-                            const float p1 = ex2(fmaf(__uint_as_float(d[e + 1]), q.z, -q.w));
-                            sum.x += this_tok < row_lim[c0 + b + e] ? p0 : 0.f;
-                            sum.y += this_tok < row_lim[c0 + b + e + 1] ? p1 : 0.f;
-                        }
+                for (int y = 0; y < kBatch; ++y) {
+                    const int r = rb + y * kStep, gr = r0 + r;
+                    x0[y] = x1[y] = make_uint2(0u, 0u);
+                    lse[y] = -INFINITY;
+                    if (r < n_rows) {
+                        const int64_t qrow = ((int64_t)s * a.M + gr / G) * a.H_q + h * G + gr % G;
+                        const uint2* src = reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim);
+                        x0[y] = __ldca(src + 8 * i0 + p);
+                        x1[y] = __ldca(src + 8 * (i0 + 1) + p);
+                        lse[y] = __ldca(a.lse + qrow);
                     }
                 }
-                w += sum.x + sum.y;
+#pragma unroll
+                for (int y = 0; y < kBatch; ++y) {
+                    const int r = rb + y * kStep;
+                    if (r >= n_pad) break;  // the same for a whole warp: n_pad is a multiple of 16
+                    const uint32_t w[4] = {x0[y].x, x0[y].y, x1[y].x, x1[y].y};
+                    float mx = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const int e2 = row_exponent(mx);
+                    const float down = pow2(-e2);
+                    uint32_t f[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+                    *reinterpret_cast<uint4*>(qs + (m >> 3) * (kTcRows * 128) + r * 128 + (((m & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(f[0], f[1], f[2], f[3]);
+                    if (m == 0) {
+                        // a row that attended to nothing adds nothing
+                        const bool counts = lse[y] > -INFINITY || lse[y] != lse[y];
+                        float* rp = reinterpret_cast<float*>(row_p + r / 2) + (r & 1);
+                        rp[0] = counts ? a.scale_log2 * pow2(e2) : 0.f;
+                        rp[2] = counts ? -lse[y] * kLog2e : -INFINITY;
+                        row_lim[r] = counts ? len - a.M + (r0 + r) / G + 1 : 0;
+                        if (!counts && r < n_rows) chunk_plain[r / kTcChunk] = 0;
+                    }
+                }
             }
-            if (real && alive) a.acc_out[this_row] = before + w;
+            fence_proxy_async_smem();
+            __syncthreads();
+
+            const float* acc_from = r0 ? a.acc_out : a.acc_in;
+            const uint64_t db = tc::smem_desc(smem_u32(qs), 1024);
+            for (int x = 0; x < mine; ++x) {
+                // ---- keys of `next` to the A operand (a strip that is not there leaves what `next` held: its
+                // tokens are not written) ----
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t f[8][4], v[32];
+                    next[half].operand(f);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {  // columns 8ks + 2i, + 1 of rows tr and tr + 8
+                        v[4 * ks] = f[ks][0];
+                        v[4 * ks + 1] = f[ks][2];
+                        v[4 * ks + 2] = f[ks][1];
+                        v[4 * ks + 3] = f[ks][3];
+                    }
+                    tc::st_16x256b_x8(tm + my_lanes + ((uint32_t)(16 * half) << 16), v);
+                }
+                const int64_t this_row = from + lane;
+                const int this_tok = from_tok + lane;
+                const bool real = from >= 0 && this_tok < len;
+                const float before = real ? acc_from[this_row] : 0.f;
+                if (x + 1 < mine) fetch(x + 1);
+                tc::wait_st();
+                float w = 0.f;
+                for (int c0 = 0; c0 < n_rows; c0 += kTcChunk) {
+                    const int n = min(kTcChunk, n_pad - c0);
+                    // every thread of the group has stored its keys and read its logits of the chunk before
+                    tc::fence_before();
+                    asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
+                    if ((tid & 127) == 0 && alive) {
+                        tc::fence_after();
+                        const uint32_t id = tc::idesc(128, n, false);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            tc::mma_ts(tm + 64, tm + 8 * kk,
+                                       db + (uint64_t)(((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32 + c0 * 128) >> 4), id, kk > 0);
+                        tc::commit(&done[group]);
+                    }
+                    // a wait that ran out leaves the thread to the barriers only
+                    if (alive) alive = mbar_wait(&done[group], phase, a.status);
+                    phase ^= 1;
+                    tc::fence_after();
+                    const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, this_tok < first_hidden);
+                    float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                    for (int b = 0; b < kTcChunk; b += 16) {
+                        if (b >= n) break;
+                        uint32_t d[16];
+                        tc::ld16(tm + 64 + my_lanes + b, d);
+                        tc::wait_ld();
+                        const float4* rp = row_p + (c0 + b) / 2;
+                        auto weigh = [&](auto masked) {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                const float4 q = rp[e >> 1];
+                                float2 p = fma2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])),
+                                                make_float2(q.x, q.y), make_float2(q.z, q.w));
+                                p.x = ex2(p.x);
+                                p.y = ex2(p.y);
+                                if (decltype(masked)::value) {
+                                    if (this_tok >= row_lim[c0 + b + e]) p.x = 0.f;
+                                    if (this_tok >= row_lim[c0 + b + e + 1]) p.y = 0.f;
+                                }
+                                if (e & 2)
+                                    sum1 = add2(sum1, p);
+                                else
+                                    sum0 = add2(sum0, p);
+                            }
+                        };
+                        if (all_seen)
+                            weigh(std::false_type{});
+                        else
+                            weigh(std::true_type{});
+                    }
+                    const float2 sum = add2(sum0, sum1);
+                    w += sum.x + sum.y;
+                }
+                if (real && alive) a.acc_out[this_row] = before + w;
+            }
         }
     }
     if (!alive && (tid & 127) == 0) mbar_wait(&done[group], phase ^ 1, a.status);  // products still in flight
@@ -518,6 +572,7 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     a.block_table = c.block_table;
     a.seq_lens = c.seq_lens;
     a.status = c.status;
+    a.B = c.B;
     a.H_q = c.H_q;
     a.H_kv = c.H_kv;
     a.b = c.b;
@@ -536,10 +591,10 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     a.acc_out = acc_out;
     if (kFour && a.rows >= kTcLeastRows) {
         if (allow_smem<accumulate_weights_tc_kernel>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
+        // every CTA that fits (two an SM) once, and at least one tile a warpgroup
         const int64_t tiles = ((int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kStripTokens) + 3) / 4;
-        const int64_t most = (tiles + kTcGroups - 1) / kTcGroups, want = 4 * 2 * 148 / ((int64_t)c.B * c.H_kv);
-        const int64_t x = want < 1 ? 1 : want;
-        dim3 grid((unsigned)(x < most ? x : most < 1 ? 1 : most), c.H_kv, c.B);
+        const int64_t most = (tiles * c.B * c.H_kv + kTcGroups - 1) / kTcGroups;
+        dim3 grid((unsigned)(most < 1 ? 1 : most < 2 * 148 ? most : 2 * 148));
         return launch(accumulate_weights_tc_kernel, grid, dim3(kTcThreads), kTcSmem, stream, a);
     }
     // one tile a warp at least; up to eight CTAs per SM's worth of them, so ragged lengths even out
