@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     __shared__ uint64_t done[kTcGroups];
     __shared__ uint32_t tmem_at;
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = tid >> 7;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = a.H_q / a.H_kv, spb = a.b / kStripTokens;
     if (tid == 0) {
         for (int i = 0; i < kTcGroups; ++i) mbar_init(&done[i], 1);
@@ -371,7 +371,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    const uint32_t tm = tmem_at + group * kTcGroupCols, my_lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t uwarp = tc::uniform(warp), group = uwarp >> 2;
+    const uint32_t tm = tc::uniform(tmem_at) + group * kTcGroupCols, my_lanes = (uint32_t)(32 * (uwarp & 3)) << 16;
+    const bool issuer = (uwarp & 3) == 0;  // the group's warp that issues its products
     uint32_t phase = 0;
     bool alive = true;
 
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
         const int32_t* sel = a.sel_idx ? a.sel_idx + (int64_t)unit * a.n_max : nullptr;
         const int t0 = (int)at, n_tiles = min(left, (nb * spb + 3) / 4 - t0);
         left -= n_tiles;
-        const int mine = group < n_tiles ? (n_tiles - group + kTcGroups - 1) / kTcGroups : 0;
+        const int mine = (int)group < n_tiles ? (n_tiles - (int)group + kTcGroups - 1) / kTcGroups : 0;
         const int first_hidden = len - a.M + 1;
 
         int64_t row = -1;
@@ -390,7 +392,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
             row = -1;
             tok = 0;
             if (x >= mine) return;
-            const int g = 4 * (t0 + group + kTcGroups * x) + (warp & 3), pos = g / spb;
+            const int g = 4 * (t0 + (int)group + kTcGroups * x) + (warp & 3), pos = g / spb;
             if (pos >= nb) return;
             const int j = sel ? __ldca(sel + pos) : pos;
             if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
             __syncthreads();
 
             const float* acc_from = r0 ? a.acc_out : a.acc_in;
-            const uint64_t db = tc::smem_desc(smem_u32(qs), 1024);
+            const uint64_t db = tc::smem_desc(tc::uniform(smem_u32(qs)), 1024);
             for (int x = 0; x < mine; ++x) {
                 // ---- keys of `next` to the A operand (a strip that is not there leaves what `next` held: its
                 // tokens are not written) ----
@@ -502,14 +504,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                     // every thread of the group has stored its keys and read its logits of the chunk before
                     tc::fence_before();
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                    if ((tid & 127) == 0 && alive) {
+                    if (issuer && __all_sync(0xffffffffu, alive)) {
                         tc::fence_after();
-                        const uint32_t id = tc::idesc(128, n, false);
+                        const uint32_t id = tc::idesc(128, n, false), step = (uint32_t)c0 * 128 >> 4;
+                        if (tc::elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            tc::mma_ts(tm + 64, tm + 8 * kk,
-                                       db + (uint64_t)(((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32 + c0 * 128) >> 4), id, kk > 0);
-                        tc::commit(&done[group]);
+                            for (int kk = 0; kk < 8; ++kk)
+                                tc::mma_ts(tm + 64, tm + 8 * kk,
+                                           db + (step + (((kk >> 2) * (kTcRows * 128) + (kk & 3) * 32) >> 4)), id, kk > 0);
+                            tc::commit(&done[group]);
+                        }
+                        __syncwarp();
                     }
                     // a wait that ran out leaves the thread to the barriers only
                     if (alive) alive = mbar_wait(&done[group], phase, a.status);
@@ -518,23 +523,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                     const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, this_tok < first_hidden);
                     float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-                    for (int b = 0; b < kTcChunk; b += 16) {
+                    for (int b = 0; b < kTcChunk; b += 32) {
                         if (b >= n) break;
-                        uint32_t d[16];
-                        tc::ld16(tm + 64 + my_lanes + b, d);
+                        // (a chunk of 16 or 48 rows reads 16 columns more than it wrote: what they hold is not used)
+                        uint32_t d[32];
+                        tc::ld32(tm + 64 + my_lanes + b, d);
                         tc::wait_ld();
-                        const float4* rp = row_p + (c0 + b) / 2;
-                        auto weigh = [&](auto masked) {
+                        auto weigh = [&](auto masked, int e0) {
+                            const float4* rp = row_p + (c0 + b + e0) / 2;
 #pragma unroll
                             for (int e = 0; e < 16; e += 2) {
                                 const float4 q = rp[e >> 1];
-                                float2 p = fma2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])),
+                                float2 p = fma2(make_float2(__uint_as_float(d[e0 + e]), __uint_as_float(d[e0 + e + 1])),
                                                 make_float2(q.x, q.y), make_float2(q.z, q.w));
                                 p.x = ex2(p.x);
                                 p.y = ex2(p.y);
                                 if (decltype(masked)::value) {
-                                    if (this_tok >= row_lim[c0 + b + e]) p.x = 0.f;
-                                    if (this_tok >= row_lim[c0 + b + e + 1]) p.y = 0.f;
+                                    if (this_tok >= row_lim[c0 + b + e0 + e]) p.x = 0.f;
+                                    if (this_tok >= row_lim[c0 + b + e0 + e + 1]) p.y = 0.f;
                                 }
                                 if (e & 2)
                                     sum1 = add2(sum1, p);
@@ -542,10 +548,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                                     sum0 = add2(sum0, p);
                             }
                         };
-                        if (all_seen)
-                            weigh(std::false_type{});
-                        else
-                            weigh(std::true_type{});
+                        if (all_seen) {
+                            weigh(std::false_type{}, 0);
+                            if (b + 16 < n) weigh(std::false_type{}, 16);
+                        } else {
+                            weigh(std::true_type{}, 0);
+                            if (b + 16 < n) weigh(std::true_type{}, 16);
+                        }
                     }
                     const float2 sum = add2(sum0, sum1);
                     w += sum.x + sum.y;
@@ -554,7 +563,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
             }
         }
     }
-    if (!alive && (tid & 127) == 0) mbar_wait(&done[group], phase ^ 1, a.status);  // products still in flight
+    if (!alive && issuer) mbar_wait(&done[group], phase ^ 1, a.status);  // products still in flight
     tc::fence_before();
     __syncthreads();
     if (warp == 0) {
