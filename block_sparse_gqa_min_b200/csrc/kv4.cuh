@@ -49,6 +49,50 @@ __device__ __forceinline__ uint4 ld_once_v4(const void* p) {
     return v;
 }
 
+// An equal share of all the units' work for each of `ctas` CTAs, whatever the units' lengths: units are
+// laid end to end (unit u has work(u) >= 0 pieces), and CTA c takes pieces [all*c/ctas, all*(c+1)/ctas).
+// ctas(all) says among how many CTAs the work is shared, the others get none.  By one whole warp.
+struct Share {
+    int64_t all;    // pieces of all units
+    int64_t start;  // first piece of this share
+    int left;       // pieces of it
+    int ctas;
+    int unit, at;   // the first piece: its unit, and its place in that unit
+};
+template <class Work, class Ctas>
+__device__ __forceinline__ Share share_of(int units, int cta, int lane, Work work, Ctas ctas) {
+    Share r;
+    const int first = lane < units ? work(lane) : 0;
+    int64_t all = first;
+    for (int u = 32 + lane; u < units; u += 32) all += work(u);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    r.all = all;
+    r.ctas = ctas(all);
+    r.start = cta < r.ctas ? all * cta / r.ctas : all;
+    r.left = cta < r.ctas ? (int)(all * (cta + 1) / r.ctas - r.start) : 0;
+    r.unit = r.at = 0;
+    if (r.left == 0) return r;
+    int64_t at = r.start;
+    for (;; r.unit += 32) {
+        const int mine = r.unit == 0 ? first : r.unit + lane < units ? work(r.unit + lane) : 0;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, at < upto);
+        if (past) {
+            const int x = __ffs(past) - 1;
+            r.unit += x;
+            r.at = (int)(at - __shfl_sync(0xffffffffu, upto - mine, x));
+            return r;
+        }
+        at -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+}
+
 // 2^x; results below the normal range become 0.
 __device__ __forceinline__ float ex2(float x) {
     float y;

@@ -40,8 +40,10 @@ constexpr int kStages = 3;
 constexpr int kRing = kWarps * kStages * kStripBytes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMostParts = 128;           // of one unit: the merge of more would take longer than they save
+constexpr int kMergePer = 10;              // parts a lane takes in: 320 >= CTAs of a launch
 constexpr int kRowStride = kHeadDim + 4;  // floats between rows of the merge buffer
-constexpr float kPShift = 8.f;            // P is exp2(s - max + 8): small weights stay normal f16 numbers
+constexpr float kPShift = 8.f;            // P is exp2((s - max) * scale + 8): small weights stay normal f16 numbers
 constexpr float kSlack = 7.f;             // the running maximum moves only when exceeded by 2^7 (P <= 2^15)
 
 struct Args {
@@ -49,19 +51,19 @@ struct Args {
     const int32_t* block_table;
     const int32_t* seq_lens;
     int32_t* status;
-    int H_q, H_kv, b, max_blocks, num_pages, M, rows;  // rows = M * G
+    int B, H_q, H_kv, b, max_blocks, num_pages, M, rows;  // rows = M * G
     const __nv_bfloat16* q;
     const int32_t* sel_idx;
     const int32_t* sel_cnt;
     int n_max;
     float scale_log2;  // softmax scale * log2(e)
-    int splits, row_groups;
+    int row_groups;
     void* out;
     int out_bf16;
     float* lse_out;
-    uint32_t* counters;  // [B][H_kv * row_groups]
-    float* part_ml;      // [unit][split][R][2]
-    float* part_o;       // [unit][split][R][128], unnormalised
+    uint32_t* counters;  // [unit], a unit being one (sequence, KV head, row group)
+    float* part_ml;      // [part][R][2]; parts: [unit][CTA of it], or (equal shares) [CTA][its first unit's, its last's]
+    float* part_o;       // [part][R][128], unnormalised
 };
 
 // Row r of an MMA tile of 16 tokens holds token perm(r): lane i of a quad then finds the four tokens
@@ -84,9 +86,11 @@ template <int NH>
 struct State {
     float o[NH][8][4];  // O^T: [row tile][channel pair mt]: channels 16(lane/4) + 2mt (c0, c1) and + 1 (c2, c3) of
                         // rows 8nh + 2(lane%4) + x
-    float m[NH][2], l[NH][2];
-    float sc[NH][2];   // softmax scale * log2(e) * 2^e of the row
-    int lim[NH][2];    // tokens the row sees
+    float m[NH][2];     // running maximum of the unscaled logits
+    float l[NH][2];     // this lane's part of the sums
+    float high[NH][2];  // unscaled logit past which the maximum moves
+    float sc[NH][2];    // softmax scale * log2(e) * 2^e of the row
+    int lim[NH][2];     // tokens the row sees
 };
 
 template <int NH, bool kSplitP>
@@ -120,49 +124,61 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
         fence_proxy_async_smem();
         __syncwarp();
     }
-    // ---- S^T = K Q^T: two tiles of 16 tokens ----
+    // ---- S^T = K Q^T: two tiles of 16 tokens, a chain of eight MMAs each ----
     float s[NH][2][4];
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-        const int ra = 16 * mt + perm(tr), rb = 16 * mt + perm(tr + 8);
-        const uint4 ka = *reinterpret_cast<const uint4*>(strip + ra * 64 + i * 16);
-        const uint4 kb = *reinterpret_cast<const uint4*>(strip + rb * 64 + i * 16);
-        const uint32_t sa = *reinterpret_cast<const uint16_t*>(strip + kStripKS + ra * 8 + 2 * i);
-        const uint32_t sb = *reinterpret_cast<const uint16_t*>(strip + kStripKS + rb * 8 + 2 * i);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-        const uint32_t fa[2] = {scale_f16x2(sa & 0xff), scale_f16x2(sa >> 8)};
-        const uint32_t fb[2] = {scale_f16x2(sb & 0xff), scale_f16x2(sb >> 8)};
-        float even[NH][4], odd[NH][4];  // two independent accumulator chains
+    for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int x = 0; x < 4; ++x) even[nh][x] = odd[nh][x] = 0.f;
+            for (int x = 0; x < 4; ++x) s[nh][mt][x] = 0.f;
+    uint4 kc[2][2];
+    uint32_t kf[2][2][2];  // scales of channels 32i .. + 15 and + 16 .. of the tile's two rows
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const int r = 16 * mt + perm(tr + 8 * y);
+            kc[mt][y] = *reinterpret_cast<const uint4*>(strip + r * 64 + i * 16);
+            const uint32_t f = *reinterpret_cast<const uint16_t*>(strip + kStripKS + r * 8 + 2 * i);
+            kf[mt][y][0] = scale_f16x2(f & 0xff);
+            kf[mt][y][1] = scale_f16x2(f >> 8);
+        }
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
             uint32_t a[4], c[4];
-            codes_to_f16(wa[w], a[0], a[1], a[2], a[3]);
-            codes_to_f16(wb[w], c[0], c[1], c[2], c[3]);
+            const uint4 ka = kc[mt][0], kb = kc[mt][1];
+            codes_to_f16(w == 0 ? ka.x : w == 1 ? ka.y : w == 2 ? ka.z : ka.w, a[0], a[1], a[2], a[3]);
+            codes_to_f16(w == 0 ? kb.x : w == 1 ? kb.y : w == 2 ? kb.z : kb.w, c[0], c[1], c[2], c[3]);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                a[x] = mul_f16x2(a[x], fa[w >> 1]);
-                c[x] = mul_f16x2(c[x], fb[w >> 1]);
+                a[x] = mul_f16x2(a[x], kf[mt][0][w >> 1]);
+                c[x] = mul_f16x2(c[x], kf[mt][1][w >> 1]);
             }
             const uint32_t f0[4] = {a[0], c[0], a[1], c[1]}, f1[4] = {a[2], c[2], a[3], c[3]};
 #pragma unroll
             for (int nh = 0; nh < NH; ++nh) {
-                mma_f16_16816(even[nh], f0, qb[nh][2 * w][0], qb[nh][2 * w][1]);
-                mma_f16_16816(odd[nh], f1, qb[nh][2 * w + 1][0], qb[nh][2 * w + 1][1]);
+                mma_f16_16816(s[nh][mt], f0, qb[nh][2 * w][0], qb[nh][2 * w][1]);
+                mma_f16_16816(s[nh][mt], f1, qb[nh][2 * w + 1][0], qb[nh][2 * w + 1][1]);
             }
         }
+    // ---- masks, where some row does not see some token of the strip (rows past the real ones see all: they
+    // are not written) ----
+    if (valid < kStripTokens || first_hidden < tok0 + kStripTokens) {
 #pragma unroll
-        for (int nh = 0; nh < NH; ++nh)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int tok = tok0 + (x < 2 ? ra : rb);
-                s[nh][mt][x] = tok < st.lim[nh][x & 1] ? (even[nh][x] + odd[nh][x]) * st.sc[nh][x & 1] : -INFINITY;
+                const int tok = tok0 + 16 * mt + perm(tr + (x < 2 ? 0 : 8));
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh)
+                    if (tok >= st.lim[nh][x & 1]) s[nh][mt][x] = -INFINITY;
             }
     }
-    // ---- running maximum: moved only when some row's is exceeded by 2^kSlack ----
+    // ---- running maximum (of the unscaled logits: the scale is positive), moved only when some row's is
+    // exceeded by 2^kSlack ----
     float top[NH][2];
     bool grow = false;
 #pragma unroll
@@ -170,7 +186,7 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             top[nh][x] = fmaxf(fmaxf(s[nh][0][x], s[nh][0][2 + x]), fmaxf(s[nh][1][x], s[nh][1][2 + x]));
-            grow |= top[nh][x] > st.m[nh][x] + kSlack;
+            grow |= top[nh][x] > st.high[nh][x];
         }
     if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -182,8 +198,9 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 if (mx > st.m[nh][x]) {
-                    const float alpha = exp2f(st.m[nh][x] - mx);  // 0 from -inf
+                    const float alpha = exp2f((st.m[nh][x] - mx) * st.sc[nh][x]);  // 0 from -inf
                     st.m[nh][x] = mx;
+                    st.high[nh][x] = __fadd_rd(mx, __fdiv_rd(kSlack, st.sc[nh][x]));
                     st.l[nh][x] *= alpha;
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
@@ -197,13 +214,13 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
     uint32_t ph[NH][2][2], pl[NH][2][2];
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-        const float u0 = st.m[nh][0] == -INFINITY ? 0.f : st.m[nh][0] - kPShift;
-        const float u1 = st.m[nh][1] == -INFINITY ? 0.f : st.m[nh][1] - kPShift;
+        // (s - m) * scale, not s * scale - m: exactly 0 at the maximum, however large the logits are
+        const float u0 = st.m[nh][0] == -INFINITY ? 0.f : st.m[nh][0], u1 = st.m[nh][1] == -INFINITY ? 0.f : st.m[nh][1];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt) {
             float p[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) p[x] = ex2(s[nh][mt][x] - ((x & 1) ? u1 : u0));
+            for (int x = 0; x < 4; ++x) p[x] = ex2(fmaf(s[nh][mt][x] - ((x & 1) ? u1 : u0), st.sc[nh][x & 1], kPShift));
             st.l[nh][0] += p[0] + p[2];
             st.l[nh][1] += p[1] + p[3];
 #pragma unroll
@@ -257,7 +274,68 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
     }
 }
 
-template <int NH, bool kSplitP>
+// The rows of a unit from its parts (part 0 at row part0 of the partial buffers, part y at row0 + kStep y): the
+// thread's share of the unnormalised sums to acc, every row's maximum and sum to row_m, row_l.  `weights` has
+// room for parts * R floats (at most a part a CTA: 19 KB).  Out of line: its loads in flight take registers
+// that the strip loop needs.
+template <int R, int kStep>
+__device__ __noinline__ void merge_parts(const float* part_ml, const float* part_o, int64_t part0, int64_t row0,
+                                         int parts, float* weights, float* row_m, float* row_l, float4* acc) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto row_of = [&](int y) { return y == 0 ? part0 : row0 + (int64_t)y * kStep; };
+    for (int r = warp; r < R; r += kWarps) {
+        float2 p[kMergePer];
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int y = 0; y < kMergePer; ++y) {
+            p[y] = make_float2(-INFINITY, 0.f);
+            if (32 * y + lane < parts) p[y] = __ldcg(reinterpret_cast<const float2*>(part_ml) + row_of(32 * y + lane) + r);
+        }
+#pragma unroll
+        for (int y = 0; y < kMergePer; ++y) m = fmaxf(m, p[y].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int y = 0; y < kMergePer; ++y) {
+            const float f = p[y].y == 0.f ? 0.f : exp2f(p[y].x - m);
+            if (32 * y + lane < parts) weights[(32 * y + lane) * R + r] = f;
+            l += f * p[y].y;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (lane == 0) {
+            row_m[r] = m;
+            row_l[r] = l;
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int x = 0; x < R * 32 / kThreads; ++x) {
+        const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y0 = 0; y0 < parts; y0 += 16) {  // sixteen loads in flight
+            float4 o[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+                o[y] = __ldcg(reinterpret_cast<const float4*>(part_o + (row_of(min(y0 + y, parts - 1)) + r) * kHeadDim) + c4);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+                const float f = y0 + y < parts ? weights[(y0 + y) * R + r] : 0.f;
+                if (f != 0.f) {
+                    v.x += f * o[y].x;
+                    v.y += f * o[y].y;
+                    v.z += f * o[y].z;
+                    v.w += f * o[y].w;
+                }
+            }
+        }
+        acc[x] = v;
+    }
+}
+
+// kShared: a CTA takes an equal share of all units' strips, which may span several units; else the grid
+// is (CTAs a unit, KV heads x row groups, sequences) and a CTA works on one unit.
+template <int NH, bool kSplitP, bool kShared>
 __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(Args a) {
     constexpr int R = 8 * NH;
     extern __shared__ __align__(128) uint8_t ring[];
@@ -269,9 +347,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
     __shared__ int last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int sp = blockIdx.x, s = blockIdx.z;
-    const int h = blockIdx.y / a.row_groups, rg = blockIdx.y % a.row_groups;
-    const int G = a.H_q / a.H_kv;
+    const int G = a.H_q / a.H_kv, spb = a.b / kStripTokens;  // strips per block
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < kStages; ++i) mbar_init(&full[warp][i], 1);
@@ -281,289 +357,325 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
     pdl_wait();
     pdl_trigger();
 
-    const int spb = a.b / kStripTokens;  // strips per block
-    const int len = max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b));
-    const int N = blocks_of(len, a.b);
-    int nb = N;
-    const int32_t* sel = nullptr;
-    if (a.sel_idx) {
-        nb = __ldca(a.sel_cnt + s * a.H_kv + h);
-        if (nb < 0 || nb > a.n_max) {
-            if (tid == 0 && sp == 0) report(a.status, SBA_DEV_BAD_SELECTION);
-            nb = nb < 0 ? 0 : a.n_max;
-        }
-        sel = a.sel_idx + ((int64_t)s * a.H_kv + h) * a.n_max;
+    // ---- this CTA's share of all units' strips (a unit without any counts one, so that its rows get
+    // written); no fewer than a strip a warp, and no unit in more than kMostParts parts ----
+    auto length = [&](int s) { return max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b)); };
+    auto blocks = [&](int s, int h, int len) {
+        if (!a.sel_idx) return blocks_of(len, a.b);
+        const int n = __ldca(a.sel_cnt + s * a.H_kv + h);
+        if (n < 0 || n > a.n_max) report(a.status, SBA_DEV_BAD_SELECTION);
+        return n < 0 ? 0 : min(n, a.n_max);
+    };
+    Share share{};
+    if constexpr (kShared) {
+        const int units = a.B * a.H_kv * a.row_groups;
+        auto strips = [&](int u) {
+            u /= a.row_groups;
+            return max(1, blocks(u / a.H_kv, u % a.H_kv, a.sel_idx ? 0 : length(u / a.H_kv)) * spb);
+        };
+        share = share_of(units, blockIdx.x, lane, strips, [&](int64_t all) {
+            const int64_t n = min((all + kWarps - 1) / kWarps, (int64_t)units * kMostParts);
+            return (int)min(n, (int64_t)gridDim.x);
+        });
     }
-    const int64_t T = (int64_t)nb * spb;
-    const int s0 = (int)(T * sp / a.splits), s1 = (int)(T * (sp + 1) / a.splits);
-    const int mine = s0 + warp < s1 ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;  // strips s0 + warp + kWarps * x
     uint8_t* my_ring = ring + warp * (kStages * kStripBytes);
+    int seq = 0;        // strips this warp has been through (their stages and phases)
+    bool alive = true;  // no wait of this warp has run out
 
-    // lane x resolves this warp's strip 32 * batch + x
-    int64_t src = -1;
-    int tok = 0;
-    auto resolve = [&](int x) {
-        src = -1;
-        tok = 0;
-        if (x < mine) {
+    int64_t base = kShared ? share.start - share.at : 0;  // first strip of the unit, among all units'
+    int left = kShared ? share.left : 1, at = kShared ? share.at : 0, unit = kShared ? share.unit : 0;
+    while (left > 0) {
+        int s, h, rg = 0;
+        if constexpr (kShared) {
+            s = unit / (a.H_kv * a.row_groups);
+            h = unit / a.row_groups % a.H_kv;
+            rg = unit % a.row_groups;
+        } else {
+            s = blockIdx.z;
+            h = blockIdx.y;
+            if (a.row_groups > 1) {
+                h = blockIdx.y / a.row_groups;
+                rg = blockIdx.y % a.row_groups;
+            }
+            unit = blockIdx.z * gridDim.y + blockIdx.y;
+        }
+        const int len = length(s), N = blocks_of(len, a.b), nb = blocks(s, h, len), T = max(1, nb * spb);
+        // CTAs that work on the unit, if each works on one only
+        const int parts1 = kShared ? 0 : min((int)gridDim.x, (T + kWarps - 1) / kWarps);
+        if constexpr (!kShared) {
+            if ((int)blockIdx.x >= parts1) return;
+            at = (int)((int64_t)T * blockIdx.x / parts1);
+            left = (int)((int64_t)T * (blockIdx.x + 1) / parts1) - at;
+        }
+        const int32_t* sel = a.sel_idx ? a.sel_idx + ((int64_t)s * a.H_kv + h) * a.n_max : nullptr;
+        const int s0 = at, s1 = min(T, at + left);
+        const int mine = s0 + warp < s1 && alive ? (s1 - s0 - warp + kWarps - 1) / kWarps : 0;  // strips s0 + warp + kWarps * x
+
+        // lane x resolves this warp's strip 32 * batch + x
+        int64_t src = -1;
+        int tok = 0;
+        auto resolve = [&](int x) {
+            src = -1;
+            tok = 0;
             const int g = s0 + warp + kWarps * x;
-            const int j = sel ? __ldca(sel + g / spb) : g / spb;
-            if (j >= 0 && j < N) {
-                const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
-                tok = j * a.b + (g % spb) * kStripTokens;
-                if (page >= 0 && tok < len) src = ((page * a.H_kv + h) * spb + g % spb) * (int64_t)kStripBytes;
-            } else {
-                report(a.status, SBA_DEV_BAD_SELECTION);
-            }
-        }
-    };
-    auto issue = [&](int x) {  // strip x of this warp into its stage
-        if ((x & 31) == 0) resolve(x + lane);
-        const int64_t from = __shfl_sync(0xffffffffu, src, x & 31);
-        const int t = __shfl_sync(0xffffffffu, tok, x & 31);
-        if (lane == 0) {
-            const int stage = x % kStages;
-            info[warp][stage] = make_int2(t, from >= 0 ? min(kStripTokens, len - t) : 0);
-            if (from >= 0) {
-                mbar_arrive_expect_tx(&full[warp][stage], kStripBytes);
-                bulk_load(my_ring + stage * kStripBytes, a.kv + from, kStripBytes, &full[warp][stage]);
-            } else {
-                mbar_arrive(&full[warp][stage]);
-            }
-        }
-    };
-    for (int x = 0; x < min(mine, kStages); ++x) issue(x);
-
-    // ---- Q: row r of this row group, as f16 scaled to a maximum in [1, 2) ----
-    const int tr = lane >> 2, qi = lane & 3;
-    State<NH> st;
-    uint32_t qb[NH][8][2];
-#pragma unroll
-    for (int nh = 0; nh < NH; ++nh) {
-        const int r = rg * R + nh * 8 + tr;
-        uint4 w[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) w[x] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < a.rows) {
-            const uint4* p = reinterpret_cast<const uint4*>(
-                a.q + (((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G) * kHeadDim + 32 * qi);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = __ldca(p + x);
-        }
-        float mx = 0.f;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(ws[y])), fabsf(bf16_hi(ws[y]))));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e = row_exponent(mx);
-        const float down = pow2(-e);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                qb[nh][2 * x + (y >> 1)][y & 1] = pack_f16(bf16_lo(ws[y]) * down, bf16_hi(ws[y]) * down);
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int re = __shfl_sync(0xffffffffu, e, (2 * qi + x) * 4);
-            const int rr = rg * R + nh * 8 + 2 * qi + x;
-            st.sc[nh][x] = a.scale_log2 * pow2(re);
-            st.lim[nh][x] = rr < a.rows ? len - a.M + rr / G + 1 : 0;
-            st.m[nh][x] = -INFINITY;
-            st.l[nh][x] = 0.f;
-        }
-#pragma unroll
-        for (int mt = 0; mt < 8; ++mt) st.o[nh][mt][0] = st.o[nh][mt][1] = st.o[nh][mt][2] = st.o[nh][mt][3] = 0.f;
-    }
-
-    const int first_hidden = len - a.M + 1;  // the first token that some row does not see
-    for (int x = 0; x < mine; ++x) {
-        const int stage = x % kStages;
-        if (!mbar_wait(&full[warp][stage], (x / kStages) & 1, a.status)) {
-            // give up: nothing of this warp enters the merge, and its copies in flight get the same limit again
-            for (int y = x; y < min(mine, x + kStages); ++y) mbar_wait(&full[warp][y % kStages], (y / kStages) & 1, a.status);
-#pragma unroll
-            for (int nh = 0; nh < NH; ++nh) {
-                st.m[nh][0] = st.m[nh][1] = -INFINITY;
-                st.l[nh][0] = st.l[nh][1] = 0.f;
-            }
-            break;
-        }
-        const int2 inf = info[warp][stage];
-        if (inf.y > 0)
-            attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, inf.y, first_hidden, lane);
-        __syncwarp();
-        if (x + kStages < mine) issue(x + kStages);
-    }
-
-    // ---- merge the warps: each leaves its rows in its own ring ----
-    float* mo = reinterpret_cast<float*>(my_ring);
-    __syncwarp();
-#pragma unroll
-    for (int nh = 0; nh < NH; ++nh)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            float l = st.l[nh][x];
-            l += __shfl_xor_sync(0xffffffffu, l, 4);
-            l += __shfl_xor_sync(0xffffffffu, l, 8);
-            l += __shfl_xor_sync(0xffffffffu, l, 16);
-            const int r = nh * 8 + 2 * qi + x;
-#pragma unroll
-            for (int mt = 0; mt < 8; ++mt)
-                *reinterpret_cast<float2*>(mo + r * kRowStride + 16 * tr + 2 * mt) =
-                    make_float2(st.o[nh][mt][x], st.o[nh][mt][2 + x]);
-            if (tr == 0) {
-                ml[warp][r][0] = st.m[nh][x];
-                ml[warp][r][1] = l;
-            }
-        }
-    __syncthreads();
-    if (tid < R) {
-        float m = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w][tid][0]);
-        float l = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ml[w][tid][1] == 0.f ? 0.f : exp2f(ml[w][tid][0] - m);  // a NaN sum stays one
-            weight[w][tid] = f;
-            l += f * ml[w][tid][1];
-        }
-        row_m[tid] = m;
-        row_l[tid] = l;
-    }
-    __syncthreads();
-    const int64_t unit = ((int64_t)s * a.H_kv + h) * a.row_groups + rg;
-    float4 acc[R * 32 / kThreads];
-#pragma unroll
-    for (int x = 0; x < R * 32 / kThreads; ++x) {
-        const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = weight[w][r];
-            if (f == 0.f) continue;  // a warp that saw nothing
-            const float4 o = *reinterpret_cast<const float4*>(
-                reinterpret_cast<const float*>(ring + w * (kStages * kStripBytes)) + r * kRowStride + 4 * c4);
-            v.x += f * o.x;
-            v.y += f * o.y;
-            v.z += f * o.z;
-            v.w += f * o.w;
-        }
-        acc[x] = v;
-    }
-    if (a.splits > 1) {
-        // ---- leave the split's rows; the last CTA of the unit merges them ----
-        const int64_t at = (unit * a.splits + sp) * R;
-#pragma unroll
-        for (int x = 0; x < R * 32 / kThreads; ++x) {
-            const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
-            __stcg(reinterpret_cast<float4*>(a.part_o + (at + r) * kHeadDim) + c4, acc[x]);
-        }
-        if (tid < R) __stcg(reinterpret_cast<float2*>(a.part_ml) + at + tid, make_float2(row_m[tid], row_l[tid]));
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) last = atomicAdd(a.counters + unit, 1u) == (uint32_t)a.splits - 1;
-        __syncthreads();
-        if (!last) return;
-        __threadfence();
-        if (tid == 0) a.counters[unit] = 0u;  // ready for the next call
-        // weights of the splits, in the ring (splits * R floats fit: checked on the host)
-        float* wsp = reinterpret_cast<float*>(ring);
-        const float2* mlp = reinterpret_cast<const float2*>(a.part_ml) + unit * a.splits * R;
-        for (int r = warp; r < R; r += kWarps) {
-            float m = -INFINITY;
-            for (int x = lane; x < a.splits; x += 32) m = fmaxf(m, __ldcg(mlp + x * R + r).x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            float l = 0.f;
-            for (int x = lane; x < a.splits; x += 32) {
-                const float2 p = __ldcg(mlp + x * R + r);
-                const float f = p.y == 0.f ? 0.f : exp2f(p.x - m);
-                wsp[x * R + r] = f;
-                l += f * p.y;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (lane == 0) {
-                row_m[r] = m;
-                row_l[r] = l;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < R * 32 / kThreads; ++x) {
-            const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
-            const float4* p = reinterpret_cast<const float4*>(a.part_o + (unit * a.splits * R + r) * kHeadDim) + c4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int y = 0; y < a.splits; ++y) {
-                const float f = wsp[y * R + r];
-                const float4 o = __ldcg(p + (int64_t)y * R * (kHeadDim / 4));
-                if (f != 0.f) {
-                    v.x += f * o.x;
-                    v.y += f * o.y;
-                    v.z += f * o.z;
-                    v.w += f * o.w;
+            if (x < mine && g / spb < nb) {
+                const int j = sel ? __ldca(sel + g / spb) : g / spb;
+                if (j >= 0 && j < N) {
+                    const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
+                    tok = j * a.b + (g % spb) * kStripTokens;
+                    if (page >= 0 && tok < len) src = ((page * a.H_kv + h) * spb + g % spb) * (int64_t)kStripBytes;
+                } else {
+                    report(a.status, SBA_DEV_BAD_SELECTION);
                 }
+            }
+        };
+        auto issue = [&](int x) {  // strip x of this warp into its stage
+            if ((x & 31) == 0) resolve(x + lane);
+            const int64_t from = __shfl_sync(0xffffffffu, src, x & 31);
+            const int t = __shfl_sync(0xffffffffu, tok, x & 31);
+            if (lane == 0) {
+                const int stage = (seq + x) % kStages;
+                info[warp][stage] = make_int2(t, from >= 0 ? min(kStripTokens, len - t) : 0);
+                if (from >= 0) {
+                    mbar_arrive_expect_tx(&full[warp][stage], kStripBytes);
+                    bulk_load(my_ring + stage * kStripBytes, a.kv + from, kStripBytes, &full[warp][stage]);
+                } else {
+                    mbar_arrive(&full[warp][stage]);
+                }
+            }
+        };
+        for (int x = 0; x < min(mine, kStages); ++x) issue(x);
+
+        // ---- Q: row r of this row group, as f16 scaled to a maximum in [1, 2) ----
+        const int tr = lane >> 2, qi = lane & 3;
+        State<NH> st;
+        uint32_t qb[NH][8][2];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+            const int r = rg * R + nh * 8 + tr;
+            uint4 w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < a.rows) {
+                const uint4* p = reinterpret_cast<const uint4*>(
+                    a.q + (((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G) * kHeadDim + 32 * qi);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[x] = __ldca(p + x);
+            }
+            float mx = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(ws[y])), fabsf(bf16_hi(ws[y]))));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const int e = row_exponent(mx);
+            const float down = pow2(-e);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint32_t ws[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    qb[nh][2 * x + (y >> 1)][y & 1] = pack_f16(bf16_lo(ws[y]) * down, bf16_hi(ws[y]) * down);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int re = __shfl_sync(0xffffffffu, e, (2 * qi + x) * 4);
+                const int rr = rg * R + nh * 8 + 2 * qi + x;
+                st.sc[nh][x] = a.scale_log2 * pow2(re);
+                st.lim[nh][x] = rr < a.rows ? len - a.M + rr / G + 1 : 0;
+                st.m[nh][x] = st.high[nh][x] = -INFINITY;
+                st.l[nh][x] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) st.o[nh][mt][0] = st.o[nh][mt][1] = st.o[nh][mt][2] = st.o[nh][mt][3] = 0.f;
+        }
+
+        const int first_hidden = len - a.M + 1;  // the first token that some row does not see
+        for (int x = 0; x < mine; ++x) {
+            const int stage = (seq + x) % kStages;
+            if (!mbar_wait(&full[warp][stage], ((seq + x) / kStages) & 1, a.status)) {
+                // give up: nothing of this warp enters the merge, and its copies in flight get the same limit again
+                for (int y = seq + x; y < seq + min(mine, x + kStages); ++y)
+                    mbar_wait(&full[warp][y % kStages], (y / kStages) & 1, a.status);
+                alive = false;
+#pragma unroll
+                for (int nh = 0; nh < NH; ++nh) {
+                    st.m[nh][0] = st.m[nh][1] = -INFINITY;
+                    st.l[nh][0] = st.l[nh][1] = 0.f;
+                }
+                break;
+            }
+            const int2 inf = info[warp][stage];
+            if (inf.y > 0)
+                attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, inf.y, first_hidden, lane);
+            __syncwarp();
+            if (x + kStages < mine) issue(x + kStages);
+        }
+
+        seq += mine;
+
+        // ---- merge the warps: each leaves its rows in its own ring ----
+        float* mo = reinterpret_cast<float*>(my_ring);
+        __syncwarp();
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = st.l[nh][x];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int r = nh * 8 + 2 * qi + x;
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt)
+                    *reinterpret_cast<float2*>(mo + r * kRowStride + 16 * tr + 2 * mt) =
+                        make_float2(st.o[nh][mt][x], st.o[nh][mt][2 + x]);
+                if (tr == 0) {
+                    ml[warp][r][0] = st.m[nh][x] * st.sc[nh][x];
+                    ml[warp][r][1] = l;
+                }
+            }
+        __syncthreads();
+        if (tid < R) {
+            float m = -INFINITY;
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w][tid][0]);
+            float l = 0.f;
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ml[w][tid][1] == 0.f ? 0.f : exp2f(ml[w][tid][0] - m);  // a NaN sum stays one
+                weight[w][tid] = f;
+                l += f * ml[w][tid][1];
+            }
+            row_m[tid] = m;
+            row_l[tid] = l;
+        }
+        __syncthreads();
+        bool write = true;
+        float4 acc[R * 32 / kThreads];
+#pragma unroll
+        for (int x = 0; x < R * 32 / kThreads; ++x) {
+            const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = weight[w][r];
+                if (f == 0.f) continue;  // a warp that saw nothing
+                const float4 o = *reinterpret_cast<const float4*>(
+                    reinterpret_cast<const float*>(ring + w * (kStages * kStripBytes)) + r * kRowStride + 4 * c4);
+                v.x += f * o.x;
+                v.y += f * o.y;
+                v.z += f * o.z;
+                v.w += f * o.w;
             }
             acc[x] = v;
         }
-    }
+        if (s1 - s0 < T) {
+            // ---- a part of the unit: leave its rows; the last CTA of the unit to come merges them ----
+            const int64_t slot =
+                (kShared ? (int64_t)blockIdx.x * 2 + (share.start >= base ? 0 : 1) : (int64_t)unit * gridDim.x + blockIdx.x) * R;
 #pragma unroll
-    for (int x = 0; x < R * 32 / kThreads; ++x) {
-        const int r = (x * kThreads + tid) >> 5, c4 = tid & 31, row = rg * R + r;
-        if (row >= a.rows) continue;
-        const float l = row_l[r];
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
-        const int64_t orow = ((int64_t)s * a.M + row / G) * a.H_q + h * G + row % G;
-        const float4 v = acc[x];
-        if (a.out_bf16)
-            reinterpret_cast<uint2*>(a.out)[orow * 32 + c4] =
-                make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
-        else
-            reinterpret_cast<float4*>(a.out)[orow * 32 + c4] =
-                make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-        if (a.lse_out && c4 == 0) a.lse_out[orow] = l == 0.f ? -INFINITY : (row_m[r] - kPShift + log2f(l)) * kLn2;
+            for (int x = 0; x < R * 32 / kThreads; ++x) {
+                const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
+                __stcg(reinterpret_cast<float4*>(a.part_o + (slot + r) * kHeadDim) + c4, acc[x]);
+            }
+            if (tid < R) __stcg(reinterpret_cast<float2*>(a.part_ml) + slot + tid, make_float2(row_m[tid], row_l[tid]));
+            // the CTAs whose shares meet the unit
+            int c0 = 0, parts = parts1;
+            if constexpr (kShared) {
+                c0 = (int)(((base + 1) * share.ctas + share.all - 1) / share.all) - 1;
+                parts = (int)(((base + T) * share.ctas + share.all - 1) / share.all) - c0;
+            }
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) last = atomicAdd(a.counters + unit, 1u) == (uint32_t)parts - 1;
+            __syncthreads();
+            write = last;
+            if (write) {
+                __threadfence();
+                if (tid == 0) a.counters[unit] = 0u;  // ready for the next call
+                // a part is its CTA's first unit's, unless the CTA began before the unit (which only the first can)
+                int64_t row0 = (int64_t)unit * gridDim.x * R, part0 = row0;
+                if constexpr (kShared) {
+                    row0 = (int64_t)c0 * 2 * R;
+                    part0 = row0 + (share.all * c0 / share.ctas >= base ? 0 : R);
+                }
+                merge_parts<R, kShared ? 2 * R : R>(a.part_ml, a.part_o, part0, row0, parts, reinterpret_cast<float*>(ring),
+                               row_m, row_l, acc);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < R * 32 / kThreads; ++x) {
+            const int r = (x * kThreads + tid) >> 5, c4 = tid & 31, row = rg * R + r;
+            if (row >= a.rows || !write) continue;
+            const float l = row_l[r];
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+            const int64_t orow = ((int64_t)s * a.M + row / G) * a.H_q + h * G + row % G;
+            const float4 v = acc[x];
+            if (a.out_bf16)
+                reinterpret_cast<uint2*>(a.out)[orow * 32 + c4] =
+                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+            else
+                reinterpret_cast<float4*>(a.out)[orow * 32 + c4] =
+                    make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+            if (a.lse_out && c4 == 0) a.lse_out[orow] = l == 0.f ? -INFINITY : (row_m[r] - kPShift + log2f(l)) * kLn2;
+        }
+        if constexpr (!kShared) return;
+        left -= s1 - s0;
+        at = 0;
+        base += T;
+        ++unit;
+        // the rings go back to the copies
+        fence_proxy_async_smem();
+        __syncthreads();
     }
 }
 
 constexpr int kRefSMs = 148;
 
 struct Plan {
-    int NH, row_groups, splits;
-    size_t counters, ml, total;
+    int NH, row_groups, parts, ctas;
+    size_t ml, o, total;
 };
 
-// Splits: enough CTAs for four waves of two per SM when the sequences are long, so that ragged
-// lengths even out, but never fewer than one strip a warp.
+// Every CTA that fits once (two an SM at 8 rows, one at 16).  Few strips (at most four a warp): a CTA
+// works on one unit, which saves the search for its share.  Many: equal shares of all units' strips, so
+// that ragged lengths cost nothing.
 Plan plan_of(const sba_cache4& c, int M, int n_max) {
     Plan p;
     const int rows = M * (c.H_q / c.H_kv);
     p.NH = rows <= 8 ? 1 : 2;
     p.row_groups = (rows + 8 * p.NH - 1) / (8 * p.NH);
     const int64_t units = (int64_t)c.B * c.H_kv * p.row_groups;
-    const int64_t blocks = n_max > 0 ? n_max : (c.max_len + c.b - 1) / c.b;
-    const int64_t strips = blocks * (c.b / kStripTokens);
-    int64_t most = (strips + kWarps - 1) / kWarps;
-    int64_t want = 2 * kRefSMs / units;
-    if (strips >= 64 * kWarps) want = 8 * kRefSMs / units;
-    p.splits = (int)(want < 1 ? 1 : want > 128 ? 128 : want);
-    if (p.splits > most) p.splits = (int)(most < 1 ? 1 : most);
+    int64_t strips = (int64_t)(n_max > 0 ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kStripTokens);
+    if (strips < 1) strips = 1;
+    const int64_t fit = p.NH == 1 ? 2 * kRefSMs : kRefSMs, most = (strips + kWarps - 1) / kWarps;
+    if (units <= fit && units * strips <= fit * kWarps * 4) {
+        p.parts = (int)(fit / units < most ? fit / units : most);
+        p.ctas = (int)units * p.parts;
+    } else {
+        p.parts = 0;
+        p.ctas = (int)(units * most < fit ? units * most : fit);
+    }
     const size_t R = 8 * p.NH;
-    const size_t rows_all = p.splits > 1 ? (size_t)units * p.splits * R : 0;
-    p.counters = 0;
     p.ml = ((size_t)units * 4 + 255) / 256 * 256;
-    p.total = p.ml + rows_all * (2 + kHeadDim) * 4;
+    const size_t parts = (size_t)p.ctas * (p.parts ? 1 : 2);
+    p.o = p.ml + parts * R * 2 * 4;
+    p.total = p.o + parts * R * kHeadDim * 4;
     return p;
 }
 
-template <int NH, bool kSplitP>
-int launch_one(const Args& a, dim3 grid, cudaStream_t stream) {
-    if (allow_smem<decode_kv4_kernel<NH, kSplitP>>(kRing) != SBA_OK) return SBA_ERR_CUDA;
-    return launch(decode_kv4_kernel<NH, kSplitP>, grid, dim3(kThreads), kRing, stream, a);
+template <int NH, bool kSplitP, bool kShared>
+int launch_one(const Args& a, const Plan& p, cudaStream_t stream) {
+    if (allow_smem<decode_kv4_kernel<NH, kSplitP, kShared>>(kRing) != SBA_OK) return SBA_ERR_CUDA;
+    const dim3 grid = kShared ? dim3(p.ctas) : dim3(p.parts, a.H_kv * a.row_groups, a.B);
+    return launch(decode_kv4_kernel<NH, kSplitP, kShared>, grid, dim3(kThreads), kRing, stream, a);
+}
+
+template <int NH>
+int launch_rows(const Args& a, const Plan& p, cudaStream_t stream) {
+    if (p.parts) return a.out_bf16 ? launch_one<NH, false, false>(a, p, stream) : launch_one<NH, true, false>(a, p, stream);
+    return a.out_bf16 ? launch_one<NH, false, true>(a, p, stream) : launch_one<NH, true, true>(a, p, stream);
 }
 
 }  // namespace
@@ -579,6 +691,7 @@ int launch_decode_kv4(const sba_cache4& c, const void* q, int M, const int32_t* 
     a.block_table = c.block_table;
     a.seq_lens = c.seq_lens;
     a.status = c.status;
+    a.B = c.B;
     a.H_q = c.H_q;
     a.H_kv = c.H_kv;
     a.b = c.b;
@@ -591,18 +704,15 @@ int launch_decode_kv4(const sba_cache4& c, const void* q, int M, const int32_t* 
     a.sel_cnt = sel_cnt;
     a.n_max = n_max;
     a.scale_log2 = scale * kLog2e;
-    a.splits = p.splits;
     a.row_groups = p.row_groups;
     a.out = out;
     a.out_bf16 = out_dtype == SBA_OUT_BF16;
     a.lse_out = lse_out;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    a.counters = reinterpret_cast<uint32_t*>(w + p.counters);
+    a.counters = reinterpret_cast<uint32_t*>(w);
     a.part_ml = reinterpret_cast<float*>(w + p.ml);
-    a.part_o = a.part_ml + (size_t)c.B * c.H_kv * p.row_groups * p.splits * 8 * p.NH * 2;
-    dim3 grid(p.splits, c.H_kv * p.row_groups, c.B);
-    if (p.NH == 1) return a.out_bf16 ? launch_one<1, false>(a, grid, stream) : launch_one<1, true>(a, grid, stream);
-    return a.out_bf16 ? launch_one<2, false>(a, grid, stream) : launch_one<2, true>(a, grid, stream);
+    a.part_o = reinterpret_cast<float*>(w + p.o);
+    return p.NH == 1 ? launch_rows<1>(a, p, stream) : launch_rows<2>(a, p, stream);
 }
 
 }  // namespace sba

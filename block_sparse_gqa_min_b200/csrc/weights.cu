@@ -342,31 +342,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
         if (n < 0 || n > a.n_max) report(a.status, SBA_DEV_BAD_SELECTION);
         return n < 0 ? 0 : min(n, a.n_max);
     };
-    auto tiles = [&](int u) { return u < units ? (blocks(u) * spb + 3) / 4 : 0; };
-    int64_t all = 0;
-    for (int u = lane; u < units; u += 32) all += tiles(u);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    int64_t at = all * blockIdx.x / gridDim.x;  // first tile of the share, then within its unit
-    int left = (int)(all * (blockIdx.x + 1) / gridDim.x - at);
-    int unit = 0;
-    for (;; unit += 32) {
-        const int mine = tiles(unit + lane);
-        int upto = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += v;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, at < upto);
-        if (past || left == 0) {
-            const int x = past ? __ffs(past) - 1 : 0;
-            unit += x;
-            at -= __shfl_sync(0xffffffffu, upto - mine, x);
-            break;
-        }
-        at -= __shfl_sync(0xffffffffu, upto, 31);
-    }
+    auto tiles = [&](int u) { return (blocks(u) * spb + 3) / 4; };
+    const int ctas = gridDim.x;
+    const Share share = share_of(units, blockIdx.x, lane, tiles, [&](int64_t) { return ctas; });
+    int left = share.left, unit = share.unit, at = share.at;
 
     tc::fence_before();
     __syncthreads();
@@ -381,7 +360,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
         const int s = unit / a.H_kv, h = unit % a.H_kv;
         const int len = length(s), N = blocks_of(len, a.b), nb = blocks(unit);
         const int32_t* sel = a.sel_idx ? a.sel_idx + (int64_t)unit * a.n_max : nullptr;
-        const int t0 = (int)at, n_tiles = min(left, (nb * spb + 3) / 4 - t0);
+        const int t0 = at, n_tiles = min(left, (nb * spb + 3) / 4 - t0);
         left -= n_tiles;
         const int mine = (int)group < n_tiles ? (n_tiles - (int)group + kTcGroups - 1) / kTcGroups : 0;
         const int first_hidden = len - a.M + 1;
