@@ -41,7 +41,6 @@ constexpr int kRing = kWarps * kStages * kStripBytes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMostParts = 128;           // of one unit: the merge of more would take longer than they save
-constexpr int kMergePer = 10;              // parts a lane takes in: 320 >= CTAs of a launch
 constexpr int kRowStride = kHeadDim + 4;  // floats between rows of the merge buffer
 constexpr float kPShift = 8.f;            // P is exp2((s - max) * scale + 8): small weights stay normal f16 numbers
 constexpr float kSlack = 7.f;             // the running maximum moves only when exceeded by 2^7 (P <= 2^15)
@@ -274,63 +273,23 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
     }
 }
 
-// The rows of a unit from its parts (part 0 at row part0 of the partial buffers, part y at row0 + kStep y): the
-// thread's share of the unnormalised sums to acc, every row's maximum and sum to row_m, row_l.  `weights` has
-// room for parts * R floats (at most a part a CTA: 19 KB).  Out of line: its loads in flight take registers
-// that the strip loop needs.
-template <int R, int kStep>
-__device__ __noinline__ void merge_parts(const float* part_ml, const float* part_o, int64_t part0, int64_t row0,
-                                         int parts, float* weights, float* row_m, float* row_l, float4* acc) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    auto row_of = [&](int y) { return y == 0 ? part0 : row0 + (int64_t)y * kStep; };
-    for (int r = warp; r < R; r += kWarps) {
-        float2 p[kMergePer];
-        float m = -INFINITY, l = 0.f;
+// Maximum and sum of a row whose parts' (maximum, sum) the lanes hold, and this lane's part's weight.  A part
+// that saw nothing has a sum of 0; a NaN sum stays one.
+__device__ __forceinline__ void join(float m, float l, float& weight, float& top, float& sum) {
+    top = m;
 #pragma unroll
-        for (int y = 0; y < kMergePer; ++y) {
-            p[y] = make_float2(-INFINITY, 0.f);
-            if (32 * y + lane < parts) p[y] = __ldcg(reinterpret_cast<const float2*>(part_ml) + row_of(32 * y + lane) + r);
-        }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    weight = l == 0.f ? 0.f : exp2f(m - top);
+    sum = weight * l;
 #pragma unroll
-        for (int y = 0; y < kMergePer; ++y) m = fmaxf(m, p[y].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll
-        for (int y = 0; y < kMergePer; ++y) {
-            const float f = p[y].y == 0.f ? 0.f : exp2f(p[y].x - m);
-            if (32 * y + lane < parts) weights[(32 * y + lane) * R + r] = f;
-            l += f * p[y].y;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (lane == 0) {
-            row_m[r] = m;
-            row_l[r] = l;
-        }
-    }
-    __syncthreads();
-#pragma unroll 1
-    for (int x = 0; x < R * 32 / kThreads; ++x) {
-        const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int y0 = 0; y0 < parts; y0 += 16) {  // sixteen loads in flight
-            float4 o[16];
-#pragma unroll
-            for (int y = 0; y < 16; ++y)
-                o[y] = __ldcg(reinterpret_cast<const float4*>(part_o + (row_of(min(y0 + y, parts - 1)) + r) * kHeadDim) + c4);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-                const float f = y0 + y < parts ? weights[(y0 + y) * R + r] : 0.f;
-                if (f != 0.f) {
-                    v.x += f * o[y].x;
-                    v.y += f * o[y].y;
-                    v.z += f * o[y].z;
-                    v.w += f * o[y].w;
-                }
-            }
-        }
-        acc[x] = v;
-    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+}
+
+__device__ __forceinline__ void add_weighted(float4& v, float f, float4 o) {
+    v.x = fmaf(f, o.x, v.x);
+    v.y = fmaf(f, o.y, v.y);
+    v.z = fmaf(f, o.z, v.z);
+    v.w = fmaf(f, o.w, v.w);
 }
 
 // kShared: a CTA takes an equal share of all units' strips, which may span several units; else the grid
@@ -342,8 +301,6 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ int2 info[kWarps][kStages];  // first token of the strip, valid tokens in it
     __shared__ float ml[kWarps][R][2];
-    __shared__ float weight[kWarps][R];
-    __shared__ float row_m[R], row_l[R];
     __shared__ int last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -444,24 +401,29 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
                 }
             }
         };
-        for (int x = 0; x < min(mine, kStages); ++x) issue(x);
-
-        // ---- Q: row r of this row group, as f16 scaled to a maximum in [1, 2) ----
+        // the query rows' loads go out before the strips are looked up
         const int tr = lane >> 2, qi = lane & 3;
-        State<NH> st;
-        uint32_t qb[NH][8][2];
+        uint4 qw[NH][4];
 #pragma unroll
         for (int nh = 0; nh < NH; ++nh) {
             const int r = rg * R + nh * 8 + tr;
-            uint4 w[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = make_uint4(0u, 0u, 0u, 0u);
+            for (int x = 0; x < 4; ++x) qw[nh][x] = make_uint4(0u, 0u, 0u, 0u);
             if (r < a.rows) {
                 const uint4* p = reinterpret_cast<const uint4*>(
                     a.q + (((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G) * kHeadDim + 32 * qi);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) w[x] = __ldca(p + x);
+                for (int x = 0; x < 4; ++x) qw[nh][x] = __ldca(p + x);
             }
+        }
+        for (int x = 0; x < min(mine, kStages); ++x) issue(x);
+
+        // ---- Q: row r of this row group, as f16 scaled to a maximum in [1, 2) ----
+        State<NH> st;
+        uint32_t qb[NH][8][2];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+            const uint4 (&w)[4] = qw[nh];
             float mx = 0.f;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -539,47 +501,35 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
                 }
             }
         __syncthreads();
-        if (tid < R) {
-            float m = -INFINITY;
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w][tid][0]);
-            float l = 0.f;
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ml[w][tid][1] == 0.f ? 0.f : exp2f(ml[w][tid][0] - m);  // a NaN sum stays one
-                weight[w][tid] = f;
-                l += f * ml[w][tid][1];
-            }
-            row_m[tid] = m;
-            row_l[tid] = l;
-        }
-        __syncthreads();
+        // a warp takes row 8x + warp, a lane four of its channels
         bool write = true;
-        float4 acc[R * 32 / kThreads];
+        float4 acc[NH];
+        float row_m[NH], row_l[NH];
 #pragma unroll
-        for (int x = 0; x < R * 32 / kThreads; ++x) {
-            const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int x = 0; x < NH; ++x) {
+            const int r = 8 * x + warp;
+            float f;
+            join(lane < kWarps ? ml[lane % kWarps][r][0] : -INFINITY, lane < kWarps ? ml[lane % kWarps][r][1] : 0.f, f,
+                 row_m[x], row_l[x]);
+            acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float f = weight[w][r];
-                if (f == 0.f) continue;  // a warp that saw nothing
-                const float4 o = *reinterpret_cast<const float4*>(
-                    reinterpret_cast<const float*>(ring + w * (kStages * kStripBytes)) + r * kRowStride + 4 * c4);
-                v.x += f * o.x;
-                v.y += f * o.y;
-                v.z += f * o.z;
-                v.w += f * o.w;
+                const float fw = __shfl_sync(0xffffffffu, f, w);
+                if (fw != 0.f)  // (a warp without strips left its ring as it was)
+                    add_weighted(acc[x], fw, *reinterpret_cast<const float4*>(
+                        reinterpret_cast<const float*>(ring + w * (kStages * kStripBytes)) + r * kRowStride + 4 * lane));
             }
-            acc[x] = v;
         }
         if (s1 - s0 < T) {
             // ---- a part of the unit: leave its rows; the last CTA of the unit to come merges them ----
             const int64_t slot =
                 (kShared ? (int64_t)blockIdx.x * 2 + (share.start >= base ? 0 : 1) : (int64_t)unit * gridDim.x + blockIdx.x) * R;
 #pragma unroll
-            for (int x = 0; x < R * 32 / kThreads; ++x) {
-                const int r = (x * kThreads + tid) >> 5, c4 = tid & 31;
-                __stcg(reinterpret_cast<float4*>(a.part_o + (slot + r) * kHeadDim) + c4, acc[x]);
+            for (int x = 0; x < NH; ++x) {
+                const int64_t at_row = slot + 8 * x + warp;
+                __stcg(reinterpret_cast<float4*>(a.part_o + at_row * kHeadDim) + lane, acc[x]);
+                if (lane == 0) __stcg(reinterpret_cast<float2*>(a.part_ml) + at_row, make_float2(row_m[x], row_l[x]));
             }
-            if (tid < R) __stcg(reinterpret_cast<float2*>(a.part_ml) + slot + tid, make_float2(row_m[tid], row_l[tid]));
             // the CTAs whose shares meet the unit
             int c0 = 0, parts = parts1;
             if constexpr (kShared) {
@@ -594,31 +544,75 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             if (write) {
                 __threadfence();
                 if (tid == 0) a.counters[unit] = 0u;  // ready for the next call
-                // a part is its CTA's first unit's, unless the CTA began before the unit (which only the first can)
+                // part y's rows; a part is its CTA's first unit's, unless the CTA began before the unit (only the first can)
+                constexpr int kStep = kShared ? 2 * R : R;
                 int64_t row0 = (int64_t)unit * gridDim.x * R, part0 = row0;
                 if constexpr (kShared) {
                     row0 = (int64_t)c0 * 2 * R;
                     part0 = row0 + (share.all * c0 / share.ctas >= base ? 0 : R);
                 }
-                merge_parts<R, kShared ? 2 * R : R>(a.part_ml, a.part_o, part0, row0, parts, reinterpret_cast<float*>(ring),
-                               row_m, row_l, acc);
+                auto row_of = [&](int y) { return y == 0 ? part0 : row0 + (int64_t)y * kStep; };
+                float* weights = reinterpret_cast<float*>(my_ring);  // the parts': at most one a CTA
+#pragma unroll 1
+                for (int x = 0; x < NH; ++x) {
+                    const int r = 8 * x + warp;
+                    const float2* mlp = reinterpret_cast<const float2*>(a.part_ml) + r;
+                    float m = -INFINITY, l = 0.f;
+                    if (parts <= 32) {
+                        float2 p = make_float2(-INFINITY, 0.f);
+                        if (lane < parts) p = __ldcg(mlp + row_of(lane));
+                        float f;
+                        join(p.x, p.y, f, m, l);
+                        weights[lane] = f;
+                    } else {
+                        for (int y = lane; y < parts; y += 32) m = fmaxf(m, __ldcg(mlp + row_of(y)).x);
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        for (int y = lane; y < parts; y += 32) {
+                            const float2 p = __ldcg(mlp + row_of(y));
+                            const float f = p.y == 0.f ? 0.f : exp2f(p.x - m);
+                            weights[y] = f;
+                            l += f * p.y;
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                    }
+                    __syncwarp();
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4* op = reinterpret_cast<const float4*>(a.part_o + r * kHeadDim) + lane;
+#pragma unroll 8
+                    for (int y = 0; y < parts; ++y)
+                        add_weighted(v, weights[y], __ldcg(op + row_of(y) * (kHeadDim / 4)));
+                    __syncwarp();
+                    // (indexed with constants only, so that they stay in registers)
+                    if (x == 0) {
+                        acc[0] = v;
+                        row_m[0] = m;
+                        row_l[0] = l;
+                    } else {
+                        acc[NH - 1] = v;
+                        row_m[NH - 1] = m;
+                        row_l[NH - 1] = l;
+                    }
+                }
             }
         }
 #pragma unroll
-        for (int x = 0; x < R * 32 / kThreads; ++x) {
-            const int r = (x * kThreads + tid) >> 5, c4 = tid & 31, row = rg * R + r;
+        for (int x = 0; x < NH; ++x) {
+            const int row = rg * R + 8 * x + warp;
             if (row >= a.rows || !write) continue;
-            const float l = row_l[r];
+            const float l = row_l[x];
             const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
             const int64_t orow = ((int64_t)s * a.M + row / G) * a.H_q + h * G + row % G;
             const float4 v = acc[x];
             if (a.out_bf16)
-                reinterpret_cast<uint2*>(a.out)[orow * 32 + c4] =
+                reinterpret_cast<uint2*>(a.out)[orow * 32 + lane] =
                     make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
             else
-                reinterpret_cast<float4*>(a.out)[orow * 32 + c4] =
+                reinterpret_cast<float4*>(a.out)[orow * 32 + lane] =
                     make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-            if (a.lse_out && c4 == 0) a.lse_out[orow] = l == 0.f ? -INFINITY : (row_m[r] - kPShift + log2f(l)) * kLn2;
+            if (a.lse_out && lane == 0)
+                a.lse_out[orow] = l == 0.f ? -INFINITY : (row_m[x] - kPShift + log2f(l)) * kLn2;
         }
         if constexpr (!kShared) return;
         left -= s1 - s0;
