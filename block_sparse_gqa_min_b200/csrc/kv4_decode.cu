@@ -73,6 +73,14 @@ __device__ __forceinline__ int perm(int r) {
     return 4 * i + (r >> 3) * 2 + ((r & 1) ^ (i & 1));
 }
 
+// CTAs of a unit of T strips that has CTAs of its own: a strip a warp (a second round costs 1 us), but no
+// more than 32 (the last CTA merges up to 32 parts in one go; 52 parts of one strip a warp took 13.8 us
+// where 26 of two take 11.0).
+__host__ __device__ __forceinline__ int64_t parts_of(int64_t T) {
+    const int64_t most = (T + kWarps - 1) / kWarps, rounds = (most + 31) / 32;
+    return (T + kWarps * rounds - 1) / (kWarps * rounds);
+}
+
 // One strip from global memory into `dst`, completing on `bar` (16-byte aligned both sides).
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
         }
         const int len = length(s), N = blocks_of(len, a.b), nb = blocks(s, h, len), T = max(1, nb * spb);
         // CTAs that work on the unit, if each works on one only
-        const int parts1 = kShared ? 0 : min((int)gridDim.x, (T + kWarps - 1) / kWarps);
+        const int parts1 = kShared ? 0 : min((int)gridDim.x, (int)parts_of(T));
         if constexpr (!kShared) {
             if ((int)blockIdx.x >= parts1) return;
             at = (int)((int64_t)T * blockIdx.x / parts1);
@@ -643,13 +651,14 @@ Plan plan_of(const sba_cache4& c, int M, int n_max) {
     const int64_t units = (int64_t)c.B * c.H_kv * p.row_groups;
     int64_t strips = (int64_t)(n_max > 0 ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kStripTokens);
     if (strips < 1) strips = 1;
-    const int64_t fit = p.NH == 1 ? 2 * kRefSMs : kRefSMs, most = (strips + kWarps - 1) / kWarps;
+    const int64_t fit = p.NH == 1 ? 2 * kRefSMs : kRefSMs, most = parts_of(strips);
     if (units <= fit && units * strips <= fit * kWarps * 4) {
         p.parts = (int)(fit / units < most ? fit / units : most);
         p.ctas = (int)units * p.parts;
     } else {
         p.parts = 0;
-        p.ctas = (int)(units * most < fit ? units * most : fit);
+        p.ctas = (int)fit;
+        if (units * strips < fit * kWarps) p.ctas = (int)((units * strips + kWarps - 1) / kWarps);
     }
     const size_t R = 8 * p.NH;
     p.ml = ((size_t)units * 4 + 255) / 256 * 256;
