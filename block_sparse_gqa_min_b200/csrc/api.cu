@@ -303,6 +303,7 @@ int sba_decode_step(const sba_cache* c, const void* q, const void* k_new, const 
 
 namespace {
 
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A four-bit cache seen as a bf16 one: the same checks, and the view that scoring (which reads the
@@ -373,7 +374,7 @@ int sba_append_kv4(const sba_cache4* c, const void* k_new, const void* v_new, co
     const int rc = check_cache4(c);
     if (rc != SBA_OK) return rc;
     if (!k_new || !v_new || !pos_start || n_new < 0) return SBA_ERR_INVALID_ARG;
-    if (!aligned16(k_new) || !aligned16(v_new)) return SBA_ERR_INVALID_ARG;
+    if (!aligned32(k_new) || !aligned32(v_new)) return SBA_ERR_INVALID_ARG;
     if (n_new == 0) return SBA_OK;
     return after_launch(launch_append_kv4(*c, k_new, v_new, pos_start, n_new, static_cast<cudaStream_t>(stream)));
 }
@@ -382,7 +383,7 @@ int sba_read_kv4(const sba_cache4* c, const int32_t* pos_start, int32_t n, void*
     const int rc = check_cache4(c);
     if (rc != SBA_OK) return rc;
     if (!k_out || !v_out || !pos_start || n < 0) return SBA_ERR_INVALID_ARG;
-    if (!aligned16(k_out) || !aligned16(v_out)) return SBA_ERR_INVALID_ARG;
+    if (!aligned32(k_out) || !aligned32(v_out)) return SBA_ERR_INVALID_ARG;
     if (n == 0) return SBA_OK;
     return after_launch(launch_read_kv4(*c, pos_start, n, k_out, v_out, static_cast<cudaStream_t>(stream)));
 }

@@ -16,6 +16,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// 32 bytes that nothing here reads again, by one load (volatile: never moved above griddepcontrol.wait).
+__device__ __forceinline__ void load_once_32(const void* p, uint32_t (&v)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(p));
+}
+
 // One CTA per (touched block, KV head, sequence).  Thread t owns channels 16(t%8) .. +15 of rows
 // t/8, t/8 + 32, ...: one scale group, so a row's codes are 8 lanes x 8 bytes and a thread needs no
 // other thread's data but for the descriptors.  The block's other valid rows are read back as held,
@@ -42,6 +49,25 @@ __global__ void __launch_bounds__(kThreads) append_kv4_kernel(sba_cache4 c, cons
     if (page < 0) return;
     uint8_t* tile = static_cast<uint8_t*>(c.kv) + (page * c.H_kv + h) * (int64_t)(kRows * kStripBytes);
 
+    // every new row's loads, then the old rows' that count in the descriptor, before anything waits for them
+    uint32_t x[2][kRows][8];
+    uint2 old[kRows];
+    uint32_t old_scale[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int t = j * kBlk + i * 32 + r0;
+        old[i] = make_uint2(0u, 0u);
+        old_scale[i] = 0;
+        if (t >= p0 && t < p0 + n_new) {
+            const int64_t src = (((int64_t)s * n_new + (t - p0)) * c.H_kv + h) * 16 + 2 * g;
+            load_once_32(k_new + src, x[0][i]);
+            load_once_32(v_new + src, x[1][i]);
+        } else if (c.desc != nullptr && t < len) {
+            const uint8_t* strip = tile + i * kStripBytes;
+            old[i] = *reinterpret_cast<const uint2*>(strip + r0 * 64 + g * 8);
+            old_scale[i] = strip[kStripKS + r0 * 8 + g];
+        }
+    }
     __half2 mn[8], mx[8];
     const __half2 top = __half2half2(__ushort_as_half(0x7c00)), bottom = __half2half2(__ushort_as_half(0xfc00));
 #pragma unroll
@@ -54,35 +80,28 @@ __global__ void __launch_bounds__(kThreads) append_kv4_kernel(sba_cache4 c, cons
         uint8_t* strip = tile + i * kStripBytes;
         const int t = j * kBlk + i * 32 + r0;
         const bool is_new = t >= p0 && t < p0 + n_new;
-        const bool counts = c.desc != nullptr && t < len;
-        uint2 kc = make_uint2(0u, 0u), vc = kc;
-        uint32_t ks = 0, vs = 0;
+        uint2 kc = old[i];
+        uint32_t ks = old_scale[i];
         if (is_new) {
-            const int64_t src = (((int64_t)s * n_new + (t - p0)) * c.H_kv + h) * 16 + 2 * g;
-            const uint4 ka = __ldca(k_new + src), kb = __ldca(k_new + src + 1);
-            const uint4 va = __ldca(v_new + src), vb = __ldca(v_new + src + 1);
-            const uint32_t xk[8] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
-            const uint32_t xv[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-            quantise16(xk, kc, ks);
-            quantise16(xv, vc, vs);
+            uint2 vc;
+            uint32_t vs;
+            quantise16(x[0][i], kc, ks);
+            quantise16(x[1][i], vc, vs);
             *reinterpret_cast<uint2*>(strip + r0 * 64 + g * 8) = kc;
             *reinterpret_cast<uint2*>(strip + kStripV + r0 * 64 + g * 8) = vc;
             strip[kStripKS + r0 * 8 + g] = (uint8_t)ks;
             strip[kStripVS + r0 * 8 + g] = (uint8_t)vs;
-        } else if (counts) {
-            kc = *reinterpret_cast<const uint2*>(strip + r0 * 64 + g * 8);
-            ks = strip[kStripKS + r0 * 8 + g];
         }
-        if (counts) {
+        if (c.desc != nullptr && t < len) {
             uint32_t v[8];
             codes_to_f16(kc.x, v[0], v[1], v[2], v[3]);
             codes_to_f16(kc.y, v[4], v[5], v[6], v[7]);
             const uint32_t sc = scale_f16x2(ks);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t x = mul_f16x2(v[e], sc);
-                mn[e] = __hmin2(mn[e], *reinterpret_cast<const __half2*>(&x));
-                mx[e] = __hmax2(mx[e], *reinterpret_cast<const __half2*>(&x));
+                const uint32_t y = mul_f16x2(v[e], sc);
+                mn[e] = __hmin2(mn[e], *reinterpret_cast<const __half2*>(&y));
+                mx[e] = __hmax2(mx[e], *reinterpret_cast<const __half2*>(&y));
             }
         }
     }
@@ -115,18 +134,25 @@ __global__ void __launch_bounds__(kThreads) append_kv4_kernel(sba_cache4 c, cons
     }
 }
 
-// One CTA per (block that overlaps the window, KV head, sequence).  Thread t owns channels
-// 8(t%16) .. +7 of rows t/16, t/16 + 16, ...: 4 code bytes in, one 16-byte store out, so a row's
-// 256 bytes are written by 16 neighbouring lanes.  All loads of a tensor are issued before the
-// first of its stores.
+// 32 bytes that nothing here reads again: one store, first to leave L2.
+__device__ __forceinline__ void store_once_32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// One CTA per (block that overlaps the window, KV head, sequence).  Thread t owns one scale group (channels
+// 16(t%8) .. +15) of rows t/8, t/8 + 32, ...: 8 code bytes and a scale byte in, one 32-byte store out, so a
+// row's 256 bytes are written by 8 neighbouring lanes.  Every load of the thread is issued before its first
+// store.
 template <int kBlk>
 __global__ void __launch_bounds__(kThreads) read_kv4_kernel(sba_cache4 c, const int32_t* pos_start, int n,
                                                             uint4* k_out, uint4* v_out) {
-    constexpr int kRows = kBlk / 16;
+    constexpr int kRows = kBlk / 32;
     pdl_wait();
     pdl_trigger();
     const int s = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
-    const int ch = tid & 15, r0 = tid >> 4;
+    const int g = tid & 7, r0 = tid >> 3;
     const int p0 = __ldca(pos_start + s);
     if (p0 < 0 || (int64_t)p0 + n > (int64_t)c.max_blocks * kBlk) {
         if (tid == 0 && blockIdx.x == 0 && h == 0) report(c.status, SBA_DEV_BAD_POSITION);
@@ -137,31 +163,37 @@ __global__ void __launch_bounds__(kThreads) read_kv4_kernel(sba_cache4 c, const 
     if (j * kBlk >= end) return;
     const int64_t page = page_of(c.block_table, c.max_blocks, c.num_pages, s, j, tid == 0 ? c.status : nullptr);
     if (page < 0) return;
-    const uint8_t* tile = static_cast<const uint8_t*>(c.kv) + (page * c.H_kv + h) * (int64_t)(kBlk / 32 * kStripBytes);
+    const uint8_t* tile = static_cast<const uint8_t*>(c.kv) + (page * c.H_kv + h) * (int64_t)(kRows * kStripBytes);
+    uint2 code[2][kRows];
+    uint32_t sc[2][kRows];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        uint32_t code[kRows], sc[kRows];
+    for (int i = 0; i < kRows; ++i) {
+        const int t = j * kBlk + 32 * i + r0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int row = r0 + 16 * i, t = j * kBlk + row;
-            code[i] = sc[i] = 0;
+        for (int which = 0; which < 2; ++which) {
+            code[which][i] = make_uint2(0u, 0u);
+            sc[which][i] = 0;
             if (t >= p0 && t < end) {
-                const uint8_t* strip = tile + (row >> 5) * kStripBytes;
-                code[i] = __ldca(reinterpret_cast<const uint32_t*>(strip + which * kStripV + (row & 31) * 64 + ch * 4));
-                sc[i] = __ldca(strip + (which ? kStripVS : kStripKS) + (row & 31) * 8 + (ch >> 1));
+                const uint8_t* strip = tile + i * kStripBytes;
+                code[which][i] = __ldcs(reinterpret_cast<const uint2*>(strip + which * kStripV + r0 * 64 + g * 8));
+                sc[which][i] = __ldca(strip + (which ? kStripVS : kStripKS) + r0 * 8 + g);
             }
         }
+    }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int t = j * kBlk + r0 + 16 * i;
-            if (t < p0 || t >= end) continue;
-            uint32_t v[4];
-            codes_to_f16(code[i], v[0], v[1], v[2], v[3]);
-            const uint32_t f = scale_f16x2(sc[i]);
+    for (int i = 0; i < kRows; ++i) {
+        const int t = j * kBlk + 32 * i + r0;
+        if (t < p0 || t >= end) continue;
+        const int64_t at = (((int64_t)s * n + (t - p0)) * c.H_kv + h) * 16 + 2 * g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = f16x2_to_bf16x2(mul_f16x2(v[e], f));
-            (which ? v_out : k_out)[(((int64_t)s * n + (t - p0)) * c.H_kv + h) * 16 + ch] =
-                make_uint4(v[0], v[1], v[2], v[3]);
+        for (int which = 0; which < 2; ++which) {
+            uint32_t v[8];
+            codes_to_f16(code[which][i].x, v[0], v[1], v[2], v[3]);
+            codes_to_f16(code[which][i].y, v[4], v[5], v[6], v[7]);
+            const uint32_t f = scale_f16x2(sc[which][i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = f16x2_to_bf16x2(mul_f16x2(v[e], f));
+            store_once_32((which ? v_out : k_out) + at, v);
         }
     }
 }

@@ -438,7 +438,7 @@ int sba_decode_step(const sba_cache *c, const void *q, const void *k_new, const 
  * larger magnitudes than 61440 are held as 61440); a code is x / scale rounded to the nearest, ties to
  * the even code.  A group that holds a NaN or an infinity reads back as NaN in all 16 channels.  The
  * sign of a zero is not kept.
- * k_new, v_new  device bf16 [B][n_new][H_kv][d], pos_start device int32 [B].
+ * k_new, v_new  device bf16 [B][n_new][H_kv][d], 32-byte aligned; pos_start device int32 [B].
  * The caller advances seq_lens to include the tokens BEFORE the call; rows at or past len_s are
  * written, but count in no descriptor.  A sequence whose positions do not lie in [0, max_blocks*b)
  * reports SBA_DEV_BAD_POSITION and is left alone.  A page belongs to one sequence of a call. */
@@ -446,7 +446,7 @@ int sba_append_kv4(const sba_cache4 *c, const void *k_new, const void *v_new, co
                    int32_t n_new, void *stream);
 
 /* Read positions [pos_start[s], pos_start[s] + n) of every sequence back as bf16 rows
- * k_out, v_out [B][n][H_kv][d] (device): exactly the values the attention uses.  Rows at or past
+ * k_out, v_out [B][n][H_kv][d] (device, 32-byte aligned): exactly the values the attention uses.  Rows at or past
  * len_s, or on a bad page, are left as they were.  Positions outside [0, max_blocks*b) report
  * SBA_DEV_BAD_POSITION. */
 int sba_read_kv4(const sba_cache4 *c, const int32_t *pos_start, int32_t n, void *k_out, void *v_out, void *stream);

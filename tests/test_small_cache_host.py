@@ -138,7 +138,7 @@ def test_bad_append_and_read():
     lib = sba.load()
     ap, rd = lib.sba_append_kv4, lib.sba_read_kv4
     for k, v, pos, n in ((None, 0x6000, 0x7000, 1), (0x5000, None, 0x7000, 1), (0x5000, 0x6000, None, 1),
-                         (0x5008, 0x6000, 0x7000, 1), (0x5000, 0x6008, 0x7000, 1), (0x5000, 0x6000, 0x7000, -1)):
+                         (0x5010, 0x6000, 0x7000, 1), (0x5000, 0x6010, 0x7000, 1), (0x5000, 0x6000, 0x7000, -1)):
         assert ap(c4(), k, v, pos, n, None) == ARG
         assert rd(c4(), pos, n, k, v, None) == ARG
     assert ap(c4(), 0x5000, 0x6000, 0x7000, 0, None) == sba.SBA_OK      # nothing to do
