@@ -7,9 +7,9 @@
 //  - evict_select_kernel: one thread-block cluster per (sequence, KV head).  Every CTA reads its
 //    slice of the weights once, four tokens a load, and keeps their order-preserving 32-bit keys in
 //    shared memory (as far as they fit; the rest is read again from L2).  The threshold is found by a
-//    radix select of 11, 11 and 10 bits: a shared-memory histogram of the slice, then one cluster
-//    barrier, after which every CTA adds the cluster's histograms through distributed shared memory
-//    and finds the same digit.  A count and an ordered write follow; no position depends on an atomic.
+//    radix select, 8 bits a pass: a shared-memory histogram of the slice, then one cluster barrier,
+//    after which every CTA adds the cluster's histograms through distributed shared memory and finds
+//    the same digit (256 bins: with 2048 and a pass less, reading ten peers' bins took 6 us a pass).  A count and an ordered write follow; no position depends on an atomic.
 //  - gather kernels: one CTA per (destination block, KV head, sequence) moves the rows (whole rows,
 //    16 bytes a lane, all loads of a thread issued before its first store), the accumulators, and forms the
 //    block's Quest descriptor from the keys it holds in registers.  Bound by HBM.
@@ -28,9 +28,11 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kBins = 2048;
-constexpr int kSelFixed = 2 * kBins * 4;          // two histograms
-constexpr int kSelMaxKeys = (226 * 1024 - kSelFixed) / 4;  // keys of a slice kept in shared memory
+constexpr int kBins = 256;
+constexpr int kCopies = 8;                  // of the first histogram, by lane: most weights share few exponents
+constexpr int kCopyStride = kBins + 4;      // words: the copies of a bin in different banks
+constexpr int kSelFixed = (kCopies * kCopyStride + 3 * kBins) * 4;
+constexpr int kSelMaxKeys = (226 * 1024 - kSelFixed) / 16 * 4;  // keys of a slice kept in shared memory
 constexpr int kMoveThreads = 256;
 
 struct SelectArgs {
@@ -48,13 +50,9 @@ __device__ __forceinline__ int clamped_len(const int32_t* seq_lens, int s, int m
     return max(0, min(__ldca(seq_lens + s), max_blocks * b));
 }
 
-__device__ __forceinline__ void ld_peer_v2(uint32_t addr, uint32_t& a, uint32_t& b) {
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
-}
-
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a, int cap) {
     extern __shared__ __align__(16) uint32_t dyn[];
-    uint32_t* keys = dyn + 2 * kBins;
+    uint32_t* keys = dyn + kSelFixed / 4;
     __shared__ uint32_t scan[kSelWarps];
     __shared__ uint32_t found[2];  // digit of the threshold, tokens still to take at it
     __shared__ uint2 warp_n[kSelWarps];
@@ -63,9 +61,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int h = blockIdx.y, s = blockIdx.z;
     const uint32_t rank = cluster_rank(), C = cluster_size();
-    for (int i = tid; i < 2 * kBins; i += kSelThreads) dyn[i] = 0;
+    for (int i = tid; i < kSelFixed / 4; i += kSelThreads) dyn[i] = 0;
     pdl_wait();
-    pdl_trigger();
     const int n = clamped_len(a.seq_lens, s, a.max_blocks, a.b);
     const int keep = a.p.n_keep;
     int32_t* kept = a.kept + ((int64_t)s * a.H_kv + h) * keep;
@@ -83,12 +80,18 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     // this CTA's slice: quads of tokens [q0, q0 + nq)
     const int n4 = (n + 3) / 4;
     const int q0 = (int)((int64_t)n4 * rank / C), nq = (int)((int64_t)n4 * (rank + 1) / C) - q0;
-    // keys of quad i of the slice: 0 outside the ranked tokens, 1 for a NaN, larger for a larger weight
-    auto read_quad = [&](int i) -> uint4 {
+    // where quad i's weights are (cells fit 32 bits: a cache has fewer than 2^31 rows), -1 on a bad page
+    auto cell_of = [&](int i) -> int {
         const int t = 4 * (q0 + i), j = t >> a.log2_b;
-        const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
-        float4 w = make_float4(NAN, NAN, NAN, NAN);  // a bad page's tokens rank last
-        if (page >= 0) w = __ldca(reinterpret_cast<const float4*>(a.acc + (page * a.H_kv + h) * a.b + (t - j * a.b)));
+        const int page = a.block_table ? __ldca(a.block_table + (int64_t)s * a.max_blocks + j) : s * a.max_blocks + j;
+        return page >= 0 && page < a.num_pages ? (page * a.H_kv + h) * a.b + (t & (a.b - 1)) : -1;
+    };
+    auto weights_of = [&](int cell) {  // a bad page's tokens rank last
+        return cell >= 0 ? __ldca(reinterpret_cast<const float4*>(a.acc + cell)) : make_float4(NAN, NAN, NAN, NAN);
+    };
+    // keys of quad i: 0 outside the ranked tokens, 1 for a NaN, larger for a larger weight
+    auto keys_of = [&](int i, float4 w) {
+        const int t = 4 * (q0 + i);
         uint4 r;
         r.x = t < sink || t >= last ? 0u : w.x != w.x ? 1u : orderable_key(w.x);
         r.y = t + 1 < sink || t + 1 >= last ? 0u : w.y != w.y ? 1u : orderable_key(w.y);
@@ -97,145 +100,144 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         return r;
     };
     auto quad = [&](int i) -> uint4 {
-        return 4 * i < cap ? *reinterpret_cast<const uint4*>(keys + 4 * i) : read_quad(i);
+        return 4 * i < cap ? *reinterpret_cast<const uint4*>(keys + 4 * i) : keys_of(i, weights_of(cell_of(i)));
     };
 
     __syncthreads();
-    // ---- read the slice; histogram of the top 11 bits ----
-    constexpr int kLoads = 8;  // in flight per thread
-    for (int i0 = tid; i0 < nq; i0 += kLoads * kSelThreads) {
-        uint4 r[kLoads];
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x)
-            if (i0 + x * kSelThreads < nq) r[x] = read_quad(i0 + x * kSelThreads);
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x) {
-            const int i = i0 + x * kSelThreads;
-            if (i >= nq) break;
-            if (4 * i < cap) *reinterpret_cast<uint4*>(keys + 4 * i) = r[x];
-            if (r[x].x) atomicAdd(&dyn[r[x].x >> 21], 1u);
-            if (r[x].y) atomicAdd(&dyn[r[x].y >> 21], 1u);
-            if (r[x].z) atomicAdd(&dyn[r[x].z >> 21], 1u);
-            if (r[x].w) atomicAdd(&dyn[r[x].w >> 21], 1u);
+    // ---- read the slice; histogram of the top 8 bits ----
+    uint32_t* own = dyn + (lane & (kCopies - 1)) * kCopyStride;
+    // (asynchronous copies: what little L1 the keys leave could not hold this many loads in flight)
+    const int held = min(nq, cap / 4);
+    for (int i = tid; i < held; i += kSelThreads) {
+        const int cell = cell_of(i);
+        if (cell >= 0) {
+            cp_async_16(keys + 4 * i, a.acc + cell);
+        } else {
+            report(a.status, SBA_DEV_BAD_PAGE);
+            *reinterpret_cast<float4*>(keys + 4 * i) = weights_of(-1);
         }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // this thread's own, and it reads no other's
+#pragma unroll 4
+    for (int i = tid; i < nq; i += kSelThreads) {
+        uint4 r;
+        if (i < held) {
+            r = keys_of(i, *reinterpret_cast<const float4*>(keys + 4 * i));
+            *reinterpret_cast<uint4*>(keys + 4 * i) = r;
+        } else {
+            r = quad(i);
+        }
+        if (r.x) atomicAdd(&own[r.x >> 24], 1u);
+        if (r.y) atomicAdd(&own[r.y >> 24], 1u);
+        if (r.z) atomicAdd(&own[r.z >> 24], 1u);
+        if (r.w) atomicAdd(&own[r.w >> 24], 1u);
+    }
+    __syncthreads();
+    if (tid < kBins) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) c += dyn[x * kCopyStride + tid];
+        dyn[tid] = c;
     }
     uint32_t prefix = 0, left = (uint32_t)k;  // left: tokens to take among those whose key starts with prefix
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        uint32_t* hist = dyn + (pass & 1) * kBins;
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, top = pass == 0 ? 0 : shift + 11 - (pass == 2);
+    for (int pass = 0; pass < 4; ++pass) {
+        uint32_t* hist = pass == 0 ? dyn : dyn + kCopies * kCopyStride + (pass - 1) * kBins;
         if (pass > 0) {
-            const uint32_t mask = pass == 1 ? 2047u : 1023u;
+            const int shift = 24 - 8 * pass;
 #pragma unroll 4
             for (int i = tid; i < nq; i += kSelThreads) {
                 const uint4 r = quad(i);
-                if (r.x >> top == prefix && r.x) atomicAdd(&hist[(r.x >> shift) & mask], 1u);
-                if (r.y >> top == prefix && r.y) atomicAdd(&hist[(r.y >> shift) & mask], 1u);
-                if (r.z >> top == prefix && r.z) atomicAdd(&hist[(r.z >> shift) & mask], 1u);
-                if (r.w >> top == prefix && r.w) atomicAdd(&hist[(r.w >> shift) & mask], 1u);
+                if (r.x >> (shift + 8) == prefix && r.x) atomicAdd(&hist[(r.x >> shift) & 255u], 1u);
+                if (r.y >> (shift + 8) == prefix && r.y) atomicAdd(&hist[(r.y >> shift) & 255u], 1u);
+                if (r.z >> (shift + 8) == prefix && r.z) atomicAdd(&hist[(r.z >> shift) & 255u], 1u);
+                if (r.w >> (shift + 8) == prefix && r.w) atomicAdd(&hist[(r.w >> shift) & 255u], 1u);
             }
         }
         cluster_sync();
-        if (pass == 1)  // every CTA has read the first histogram
-            for (int i = tid; i < kBins; i += kSelThreads) dyn[i] = 0;
-        // digits from the top: thread t takes bins kBins - 1 - 2t and the one below
-        uint32_t hi = 0, lo = 0;
-        const int bin = kBins - 2 - 2 * tid;
-        uint32_t c[kMaxCluster][2];  // all loads before the first sum
+        // digits from the top: thread d of the first eight warps takes bin 255 - d
+        uint32_t mine = 0, sum = 0;
+        if (tid < kBins) {
+            uint32_t c[kMaxCluster];  // all loads before the first sum
 #pragma unroll
-        for (uint32_t r = 0; r < kMaxCluster; ++r) {
-            c[r][0] = c[r][1] = 0;
-            if (r < C) ld_peer_v2(peer_addr(&hist[bin], r), c[r][0], c[r][1]);
-        }
+            for (uint32_t r = 0; r < kMaxCluster; ++r) c[r] = r < C ? ld_peer_u32(peer_addr(&hist[kBins - 1 - tid], r)) : 0u;
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-            lo += c[r][0];
-            hi += c[r][1];
-        }
-        uint32_t sum = hi + lo;
+            for (int r = 0; r < kMaxCluster; ++r) mine += c[r];
+            sum = mine;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        if (lane == 31) scan[warp] = sum;
-        __syncthreads();
-        uint32_t before = lane < warp ? scan[lane] : 0u;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-        before += sum - hi - lo;  // tokens in higher bins
-        if (before < left && before + hi >= left) {
-            found[0] = bin + 1;
-            found[1] = left - before;
-        } else if (before + hi < left && before + hi + lo >= left) {
-            found[0] = bin;
-            found[1] = left - before - hi;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += v;
+            }
+            if (lane == 31) scan[warp] = sum;
         }
         __syncthreads();
-        prefix = (prefix << (pass == 2 ? 10 : 11)) | found[0];
+        if (tid < kBins) {
+            uint32_t before = sum - mine;  // tokens in higher bins
+#pragma unroll
+            for (int w = 0; w < kBins / 32; ++w)
+                if (w < warp) before += scan[w];
+            if (before < left && before + mine >= left) {
+                found[0] = kBins - 1 - tid;
+                found[1] = left - before;
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | found[0];
         left = found[1];
         __syncthreads();
     }
     const uint32_t T = prefix;
 
-    // ---- tokens above and at the threshold: per warp (a run of quads each), per CTA, then the CTAs before ----
-    const int w0 = (int)((int64_t)nq * warp / kSelWarps), w1 = (int)((int64_t)nq * (warp + 1) / kSelWarps);
+    // ---- tokens above and at the threshold, in order: every thread takes a run of quads (an odd number of
+    // them: its 16-byte reads then fall in different banks), so that nothing has to be counted across lanes
+    // but the threads' totals ----
+    const int per = ((nq + kSelThreads - 1) / kSelThreads) | 1;
+    const int i0 = min(nq, tid * per), i1 = min(nq, i0 + per);
     uint32_t gt = 0, eq = 0;
 #pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
+    for (int i = i0; i < i1; ++i) {
         const uint4 r = quad(i);
         gt += (r.x > T) + (r.y > T) + (r.z > T) + (r.w > T);
         eq += (r.x == T) + (r.y == T) + (r.z == T) + (r.w == T);
     }
-    gt = __reduce_add_sync(0xffffffffu, gt);
-    eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) warp_n[warp] = make_uint2(gt, eq);
-    __syncthreads();
-    if (warp == 0) {  // exclusive sums over the warps
-        const uint2 mine = warp_n[lane];
-        uint32_t g = mine.x, e = mine.y;
+    uint32_t g = gt, e = eq;  // the tokens of this thread and those before it: warp, CTA, cluster
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t vg = __shfl_up_sync(0xffffffffu, g, o), ve = __shfl_up_sync(0xffffffffu, e, o);
-            if (lane >= o) {
-                g += vg;
-                e += ve;
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t vg = __shfl_up_sync(0xffffffffu, g, o), ve = __shfl_up_sync(0xffffffffu, e, o);
+        if (lane >= o) {
+            g += vg;
+            e += ve;
+        }
+    }
+    if (lane == 31) warp_n[warp] = make_uint2(g, e);
+    __syncthreads();
+    const uint2 n_w = lane < warp ? warp_n[lane] : make_uint2(0u, 0u);
+    g += __reduce_add_sync(0xffffffffu, n_w.x) - gt;
+    e += __reduce_add_sync(0xffffffffu, n_w.y) - eq;
+    if (tid == kSelThreads - 1) total = make_uint2(g + gt, e + eq);
+    cluster_sync();
+    uint2 n_c = make_uint2(0u, 0u);
+    if (lane < rank) {
+        n_c.x = ld_peer_u32(peer_addr(&total.x, lane));
+        n_c.y = ld_peer_u32(peer_addr(&total.y, lane));
+    }
+    g += __reduce_add_sync(0xffffffffu, n_c.x);
+    e += __reduce_add_sync(0xffffffffu, n_c.y);
+    // only now: CTAs of the next kernel that come earlier take the place of a large cluster's
+    pdl_trigger();
+    if (gt + eq > 0) {
+        for (int i = i0; i < i1; ++i) {
+            const uint4 r = quad(i);
+            const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                if (v[x] < T) continue;
+                if (v[x] > T || e < left) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
+                g += v[x] > T;
+                e += v[x] == T;
             }
         }
-        warp_n[lane] = make_uint2(g - mine.x, e - mine.y);
-        if (lane == 31) total = make_uint2(g, e);
-    }
-    cluster_sync();
-    uint32_t g0 = 0, e0 = 0;
-    if (lane < rank) {
-        g0 = ld_peer_u32(peer_addr(&total.x, lane));
-        e0 = ld_peer_u32(peer_addr(&total.y, lane));
-    }
-    g0 = __reduce_add_sync(0xffffffffu, g0) + warp_n[warp].x;
-    e0 = __reduce_add_sync(0xffffffffu, e0) + warp_n[warp].y;
-    const uint32_t lower = (1u << lane) - 1u;
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint4 r = i < w1 ? quad(i) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t v[4] = {r.x, r.y, r.z, r.w};
-        uint32_t above[4], at[4], all_g = 0, all_e = 0, g = g0, e = e0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            above[x] = __ballot_sync(0xffffffffu, v[x] > T);
-            at[x] = __ballot_sync(0xffffffffu, v[x] == T);
-            g += __popc(above[x] & lower);
-            e += __popc(at[x] & lower);
-            all_g += __popc(above[x]);
-            all_e += __popc(at[x]);
-        }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            if (v[x] > T || (v[x] == T && e < left)) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
-            g += v[x] > T;
-            e += v[x] == T;
-        }
-        g0 += all_g;
-        e0 += all_e;
     }
     cluster_sync();  // no CTA leaves while another still reads its shared memory
 }
@@ -512,6 +514,13 @@ int launch_select(const Cache& src, const float* acc, const sba_evict_params& p,
     return SBA_OK;
 }
 
+// In plain stream order: launched early, its CTAs waited on the SMs that the selection left idle, and
+// evict_512k took 71 us instead of 66.
+int launch_move(void (*kernel)(MoveArgs), dim3 grid, const MoveArgs& m, cudaStream_t stream) {
+    kernel<<<grid, kMoveThreads, 0, stream>>>(m);
+    return SBA_OK;  // the caller looks at cudaGetLastError
+}
+
 template <class Cache>
 MoveArgs move_args(const Cache& src, const float* acc, const sba_evict_params& p, const Cache& dst, float* acc_dst,
                    const int32_t* kept) {
@@ -546,7 +555,7 @@ int launch_evict(const sba_cache& src, const float* acc, const sba_evict_params&
     m.k_dst = static_cast<uint8_t*>(dst.k);
     m.v_dst = static_cast<uint8_t*>(dst.v);
     dim3 grid((p.n_keep + src.b - 1) / src.b, src.H_kv, src.B);
-    return launch(src.b == 64 ? evict_move_kernel<64> : evict_move_kernel<128>, grid, dim3(kMoveThreads), 0, stream, m);
+    return launch_move(src.b == 64 ? evict_move_kernel<64> : evict_move_kernel<128>, grid, m, stream);
 }
 
 int launch_evict_kv4(const sba_cache4& src, const float* acc, const sba_evict_params& p, const sba_cache4& dst,
@@ -557,8 +566,7 @@ int launch_evict_kv4(const sba_cache4& src, const float* acc, const sba_evict_pa
     m.k_src = static_cast<const uint8_t*>(src.kv);
     m.k_dst = static_cast<uint8_t*>(dst.kv);
     dim3 grid((p.n_keep + src.b - 1) / src.b, src.H_kv, src.B);
-    return launch(src.b == 64 ? evict_move_kv4_kernel<64> : evict_move_kv4_kernel<128>, grid, dim3(kMoveThreads), 0,
-                  stream, m);
+    return launch_move(src.b == 64 ? evict_move_kv4_kernel<64> : evict_move_kv4_kernel<128>, grid, m, stream);
 }
 
 }  // namespace sba
