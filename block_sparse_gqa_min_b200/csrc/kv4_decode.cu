@@ -102,16 +102,17 @@ struct State {
 
 template <int NH, bool kSplitP>
 __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)[NH][8][2], uint8_t* strip, int tok0,
-                                             int valid, int first_hidden, int lane) {
+                                             int valid, bool partial, int first_hidden, int lane) {
     const int tr = lane >> 2, i = lane & 3;
-    if (valid < kStripTokens) {
+    // partial: some row does not see some token of the strip
+    if (partial && valid < kStripTokens) {
         // rows past the last token may hold anything: a scale of 0 makes them 0
         for (int e = lane; e < (kStripTokens - valid) * 8; e += 32)
             strip[kStripKS + valid * 8 + e] = strip[kStripVS + valid * 8 + e] = 0;
         fence_proxy_async_smem();
         __syncwarp();
     }
-    if (first_hidden < tok0 + valid) {
+    if (partial && first_hidden < tok0 + valid) {
         // some rows do not see the last tokens: a NaN among those tokens' values must reach only the
         // rows that do (0 * NaN is NaN in the product below), so it is put there by hand
         const int t0 = max(0, first_hidden - tok0);
@@ -171,9 +172,8 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
                 mma_f16_16816(s[nh][mt], f1, qb[nh][2 * w + 1][0], qb[nh][2 * w + 1][1]);
             }
         }
-    // ---- masks, where some row does not see some token of the strip (rows past the real ones see all: they
-    // are not written) ----
-    if (valid < kStripTokens || first_hidden < tok0 + kStripTokens) {
+    // ---- masks (rows past the real ones see all where nothing is masked: they are not written) ----
+    if (partial) {
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
     constexpr int R = 8 * NH;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kWarps][kStages];
-    __shared__ int2 info[kWarps][kStages];  // first token of the strip, valid tokens in it
+    __shared__ int2 info[kWarps][kStages];  // first token of the strip; valid tokens in it, negative if some row does not see all 32
     __shared__ float ml[kWarps][R][2];
     __shared__ int last;
 
@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             const int t = __shfl_sync(0xffffffffu, tok, x & 31);
             if (lane == 0) {
                 const int stage = (seq + x) % kStages;
-                info[warp][stage] = make_int2(t, from >= 0 ? min(kStripTokens, len - t) : 0);
+                const int valid = from >= 0 ? min(kStripTokens, len - t) : 0;
+                info[warp][stage] = make_int2(t, t + kStripTokens <= len - a.M + 1 ? valid : -valid);
                 if (from >= 0) {
                     mbar_arrive_expect_tx(&full[warp][stage], kStripBytes);
                     bulk_load(my_ring + stage * kStripBytes, a.kv + from, kStripBytes, &full[warp][stage]);
@@ -479,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
                 break;
             }
             const int2 inf = info[warp][stage];
-            if (inf.y > 0)
-                attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, inf.y, first_hidden, lane);
+            if (inf.y != 0)
+                attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, abs(inf.y), inf.y < 0, first_hidden, lane);
             __syncwarp();
             if (x + kStages < mine) issue(x + kStages);
         }
