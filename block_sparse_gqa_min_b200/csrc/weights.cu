@@ -113,7 +113,9 @@ struct Keys<true> {  // channels 32i .. 32i + 31: one 16-byte read a row
     static __device__ __forceinline__ int channel(int ks, int i, int half) { return 32 * i + 4 * ks + 2 * half; }
 };
 
-template <bool kFour>
+// kShared: a CTA takes an equal share of all units' tiles (a unit being one (sequence, KV head)); else the
+// grid is (CTAs a unit, KV heads, sequences).
+template <bool kFour, bool kShared>
 __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a) {
     __shared__ uint2 qf[kRowTiles][8][32];
     __shared__ float row_sc[kRowTiles * 8], row_lse[kRowTiles * 8];
@@ -122,158 +124,174 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tr = lane >> 2, qi = lane & 3;
-    const int h = blockIdx.y, s = blockIdx.z;
     const int G = a.H_q / a.H_kv;
     pdl_wait();
     pdl_trigger();
 
-    const int len = max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b));
-    const int N = blocks_of(len, a.b);
-    int nb = N;
-    const int32_t* sel = nullptr;
-    if (a.sel_idx) {
-        nb = __ldca(a.sel_cnt + s * a.H_kv + h);
-        if (nb < 0 || nb > a.n_max) {
-            if (tid == 0 && blockIdx.x == 0) report(a.status, SBA_DEV_BAD_SELECTION);
-            nb = nb < 0 ? 0 : a.n_max;
-        }
-        sel = a.sel_idx + ((int64_t)s * a.H_kv + h) * a.n_max;
-    }
     const int tpb = a.b / kTileTokens;
-    const int64_t T = (int64_t)nb * tpb;
-    const int t0 = (int)(T * blockIdx.x / gridDim.x), t1 = (int)(T * (blockIdx.x + 1) / gridDim.x);
-    if (t0 >= t1) return;
-    const int mine = t0 + warp < t1 ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
-
-    // lane x resolves this warp's tile 32 * batch + x: cache row (page, head, row) of its first token
-    int64_t row = -1;
-    int tok = 0, pos = 0;
-    auto resolve = [&](int x) {
-        row = -1;
-        if (x >= mine) return;
-        const int g = t0 + warp + kWarps * x;
-        pos = g / tpb;
-        const int j = sel ? __ldca(sel + pos) : pos;
-        // ascending: a block listed twice would be written by two warps
-        if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
-            report(a.status, SBA_DEV_BAD_SELECTION);
-            return;
-        }
-        const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
-        tok = j * a.b + (g % tpb) * kTileTokens;
-        if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % tpb) * kTileTokens;
+    auto length = [&](int s) { return max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b)); };
+    auto blocks = [&](int u, int len) {
+        if (!a.sel_idx) return blocks_of(len, a.b);
+        const int n = __ldca(a.sel_cnt + u);
+        if (n < 0 || n > a.n_max) report(a.status, SBA_DEV_BAD_SELECTION);
+        return n < 0 ? 0 : min(n, a.n_max);
     };
+    int unit = blockIdx.z * gridDim.y + blockIdx.y, at = 0, left = 1;
+    if constexpr (kShared) {
+        const int ctas = gridDim.x;
+        const Share share = share_of(
+            a.B * a.H_kv, blockIdx.x, lane, [&](int u) { return blocks(u, a.sel_idx ? 0 : length(u / a.H_kv)) * tpb; },
+            [&](int64_t) { return ctas; });
+        unit = share.unit;
+        at = share.at;
+        left = share.left;
+    }
+    while (left > 0) {
+        const int s = kShared ? unit / a.H_kv : (int)blockIdx.z, h = kShared ? unit % a.H_kv : (int)blockIdx.y;
+        const int len = length(s), N = blocks_of(len, a.b), nb = blocks(unit, len), T = nb * tpb;
+        const int32_t* sel = a.sel_idx ? a.sel_idx + (int64_t)unit * a.n_max : nullptr;
+        if constexpr (!kShared) {
+            at = (int)((int64_t)T * blockIdx.x / gridDim.x);
+            left = (int)((int64_t)T * (blockIdx.x + 1) / gridDim.x) - at;
+            if (left == 0) return;
+        }
+        const int t0 = at, t1 = min(T, at + left);
+        const int mine = t0 + warp < t1 ? (t1 - t0 - warp + kWarps - 1) / kWarps : 0;
 
-    for (int r0 = 0; r0 < a.rows; r0 += kRowTiles * 8) {
-        const int n_rows = min(kRowTiles * 8, a.rows - r0), n_tiles = (n_rows + 7) / 8;
-        // ---- the rows' operand fragments, scales, lse and limits ----
-        if (r0) __syncthreads();
-        for (int t = warp; t < n_tiles; t += kWarps) {
-            const int r = r0 + t * 8 + tr;
-            const bool real = r < a.rows;
-            const int64_t qrow = real ? ((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G : 0;
-            const __nv_bfloat16* p = a.q + qrow * kHeadDim;
-            uint32_t w[8][2];
-            float mx = 0.f;
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t v =
-                        real ? __ldca(reinterpret_cast<const uint32_t*>(p + Keys<kFour>::channel(ks, qi, half))) : 0u;
-                    w[ks][half] = v;
-                    mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(v)), fabsf(bf16_hi(v))));
-                }
-            float up = 1.f;
-            if (kFour) {  // f16 operands: the row scaled by a power of two to a maximum in [1, 2)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const int e = row_exponent(mx);
-                const float down = pow2(-e);
-                up = pow2(e);
+        // lane x resolves this warp's tile 32 * batch + x: cache row (page, head, row) of its first token
+        int64_t row = -1;
+        int tok = 0, pos = 0;
+        auto resolve = [&](int x) {
+            row = -1;
+            if (x >= mine) return;
+            const int g = t0 + warp + kWarps * x;
+            pos = g / tpb;
+            const int j = sel ? __ldca(sel + pos) : pos;
+            // ascending: a block listed twice would be written by two warps
+            if (j < 0 || j >= N || (sel && pos > 0 && __ldca(sel + pos - 1) >= j)) {
+                report(a.status, SBA_DEV_BAD_SELECTION);
+                return;
+            }
+            const int64_t page = page_of(a.block_table, a.max_blocks, a.num_pages, s, j, a.status);
+            tok = j * a.b + (g % tpb) * kTileTokens;
+            if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % tpb) * kTileTokens;
+        };
+
+        for (int r0 = 0; r0 < a.rows; r0 += kRowTiles * 8) {
+            const int n_rows = min(kRowTiles * 8, a.rows - r0), n_tiles = (n_rows + 7) / 8;
+            // ---- the rows' operand fragments, scales, lse and limits ----
+            if (kShared || r0) __syncthreads();  // the rows before are done with
+            for (int t = warp; t < n_tiles; t += kWarps) {
+                const int r = r0 + t * 8 + tr;
+                const bool real = r < a.rows;
+                const int64_t qrow = real ? ((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G : 0;
+                const __nv_bfloat16* p = a.q + qrow * kHeadDim;
+                uint32_t w[8][2];
+                float mx = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half)
-                        w[ks][half] = pack_f16(bf16_lo(w[ks][half]) * down, bf16_hi(w[ks][half]) * down);
-            }
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) qf[t][ks][lane] = make_uint2(w[ks][0], w[ks][1]);
-            const float lse = real ? __ldca(a.lse + qrow) : -INFINITY;
-            const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
-            if (qi == 0) {
-                row_sc[t * 8 + tr] = a.scale_log2 * up;
-                row_lse[t * 8 + tr] = counts ? lse * kLog2e : 0.f;
-                row_lim[t * 8 + tr] = counts ? len - a.M + r / G + 1 : 0;
-            }
-            const int all = __all_sync(0xffffffffu, counts);
-            if (lane == 0) tile_plain[t] = all;
-        }
-        __syncthreads();
-
-        const float* acc_from = r0 ? a.acc_out : a.acc_in;
-        const int first_hidden = len - a.M + 1;
-        Keys<kFour> next;
-        auto fetch = [&](int x) {
-            if ((x & 31) == 0) resolve(x + lane);
-            const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
-            if (from >= 0) next.load(a.k, from, lane);
-        };
-        int64_t cur_row = -1;
-        int cur_tok = 0, cur_pos = 0;
-        if (mine > 0) fetch(0);
-        for (int x = 0; x < mine; ++x) {
-            cur_row = __shfl_sync(0xffffffffu, row, x & 31);
-            cur_tok = __shfl_sync(0xffffffffu, tok, x & 31);
-            cur_pos = __shfl_sync(0xffffffffu, pos, x & 31);
-            uint32_t kf[8][4];
-            next.operand(kf);
-            if (x + 1 < mine) fetch(x + 1);
-            if (cur_row < 0) continue;
-            float w0 = 0.f, w1 = 0.f;
-            const bool all_seen = cur_tok + kTileTokens <= first_hidden;
-            for (int t = 0; t < n_tiles; ++t) {
-                float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int ks = 0; ks < 8; ks += 2) {
-                    const uint2 b0 = qf[t][ks][lane], b1 = qf[t][ks + 1][lane];
-                    if (kFour) {
-                        mma_f16_16816(e, kf[ks], b0.x, b0.y);
-                        mma_f16_16816(o, kf[ks + 1], b1.x, b1.y);
-                    } else {
-                        mma_bf16_16816(e, kf[ks], b0.x, b0.y);
-                        mma_bf16_16816(o, kf[ks + 1], b1.x, b1.y);
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t v =
+                            real ? __ldca(reinterpret_cast<const uint32_t*>(p + Keys<kFour>::channel(ks, qi, half))) : 0u;
+                        w[ks][half] = v;
+                        mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(v)), fabsf(bf16_hi(v))));
                     }
+                float up = 1.f;
+                if (kFour) {  // f16 operands: the row scaled by a power of two to a maximum in [1, 2)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const int e = row_exponent(mx);
+                    const float down = pow2(-e);
+                    up = pow2(e);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half)
+                            w[ks][half] = pack_f16(bf16_lo(w[ks][half]) * down, bf16_hi(w[ks][half]) * down);
                 }
-                const int r = t * 8 + 2 * qi;
-                const float2 sc = *reinterpret_cast<const float2*>(&row_sc[r]);
-                float2 off = *reinterpret_cast<const float2*>(&row_lse[r]);
-                if (a.gate_bias) {
-                    const int64_t at = ((int64_t)s * a.H_q + h * G + r0 + r) * a.n_max + cur_pos;
-                    if (r0 + r < a.rows) off.x -= __ldca(a.gate_bias + at) * kLog2e;
-                    if (r0 + r + 1 < a.rows) off.y -= __ldca(a.gate_bias + at + a.n_max) * kLog2e;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) qf[t][ks][lane] = make_uint2(w[ks][0], w[ks][1]);
+                const float lse = real ? __ldca(a.lse + qrow) : -INFINITY;
+                const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
+                if (qi == 0) {
+                    row_sc[t * 8 + tr] = a.scale_log2 * up;
+                    row_lse[t * 8 + tr] = counts ? lse * kLog2e : 0.f;
+                    row_lim[t * 8 + tr] = counts ? len - a.M + r / G + 1 : 0;
                 }
-                float p0 = ex2(fmaf(e[0] + o[0], sc.x, -off.x)), p1 = ex2(fmaf(e[1] + o[1], sc.y, -off.y));
-                float p2 = ex2(fmaf(e[2] + o[2], sc.x, -off.x)), p3 = ex2(fmaf(e[3] + o[3], sc.y, -off.y));
-                if (!all_seen || !tile_plain[t]) {
-                    const int2 lim = *reinterpret_cast<const int2*>(&row_lim[r]);
-                    if (cur_tok + tr >= lim.x) p0 = 0.f;
-                    if (cur_tok + tr >= lim.y) p1 = 0.f;
-                    if (cur_tok + tr + 8 >= lim.x) p2 = 0.f;
-                    if (cur_tok + tr + 8 >= lim.y) p3 = 0.f;
-                }
-                w0 += p0 + p1;
-                w1 += p2 + p3;
+                const int all = __all_sync(0xffffffffu, counts);
+                if (lane == 0) tile_plain[t] = all;
             }
-            w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-            w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-            w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-            w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-            if (qi < 2) {  // lane 0 of a quad writes token tr, lane 1 token tr + 8
-                const int t = tr + 8 * qi;
-                if (cur_tok + t < len) a.acc_out[cur_row + t] = acc_from[cur_row + t] + (qi ? w1 : w0);
+            __syncthreads();
+
+            const float* acc_from = r0 ? a.acc_out : a.acc_in;
+            const int first_hidden = len - a.M + 1;
+            Keys<kFour> next;
+            auto fetch = [&](int x) {
+                if ((x & 31) == 0) resolve(x + lane);
+                const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
+                if (from >= 0) next.load(a.k, from, lane);
+            };
+            int64_t cur_row = -1;
+            int cur_tok = 0, cur_pos = 0;
+            if (mine > 0) fetch(0);
+            for (int x = 0; x < mine; ++x) {
+                cur_row = __shfl_sync(0xffffffffu, row, x & 31);
+                cur_tok = __shfl_sync(0xffffffffu, tok, x & 31);
+                cur_pos = __shfl_sync(0xffffffffu, pos, x & 31);
+                uint32_t kf[8][4];
+                next.operand(kf);
+                if (x + 1 < mine) fetch(x + 1);
+                if (cur_row < 0) continue;
+                float w0 = 0.f, w1 = 0.f;
+                const bool all_seen = cur_tok + kTileTokens <= first_hidden;
+                for (int t = 0; t < n_tiles; ++t) {
+                    float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks += 2) {
+                        const uint2 b0 = qf[t][ks][lane], b1 = qf[t][ks + 1][lane];
+                        if (kFour) {
+                            mma_f16_16816(e, kf[ks], b0.x, b0.y);
+                            mma_f16_16816(o, kf[ks + 1], b1.x, b1.y);
+                        } else {
+                            mma_bf16_16816(e, kf[ks], b0.x, b0.y);
+                            mma_bf16_16816(o, kf[ks + 1], b1.x, b1.y);
+                        }
+                    }
+                    const int r = t * 8 + 2 * qi;
+                    const float2 sc = *reinterpret_cast<const float2*>(&row_sc[r]);
+                    float2 off = *reinterpret_cast<const float2*>(&row_lse[r]);
+                    if (a.gate_bias) {
+                        const int64_t at = ((int64_t)s * a.H_q + h * G + r0 + r) * a.n_max + cur_pos;
+                        if (r0 + r < a.rows) off.x -= __ldca(a.gate_bias + at) * kLog2e;
+                        if (r0 + r + 1 < a.rows) off.y -= __ldca(a.gate_bias + at + a.n_max) * kLog2e;
+                    }
+                    float p0 = ex2(fmaf(e[0] + o[0], sc.x, -off.x)), p1 = ex2(fmaf(e[1] + o[1], sc.y, -off.y));
+                    float p2 = ex2(fmaf(e[2] + o[2], sc.x, -off.x)), p3 = ex2(fmaf(e[3] + o[3], sc.y, -off.y));
+                    if (!all_seen || !tile_plain[t]) {
+                        const int2 lim = *reinterpret_cast<const int2*>(&row_lim[r]);
+                        if (cur_tok + tr >= lim.x) p0 = 0.f;
+                        if (cur_tok + tr >= lim.y) p1 = 0.f;
+                        if (cur_tok + tr + 8 >= lim.x) p2 = 0.f;
+                        if (cur_tok + tr + 8 >= lim.y) p3 = 0.f;
+                    }
+                    w0 += p0 + p1;
+                    w1 += p2 + p3;
+                }
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+                w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+                w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+                if (qi < 2) {  // lane 0 of a quad writes token tr, lane 1 token tr + 8
+                    const int t = tr + 8 * qi;
+                    if (cur_tok + t < len) a.acc_out[cur_row + t] = acc_from[cur_row + t] + (qi ? w1 : w0);
+                }
             }
         }
+        if constexpr (!kShared) return;
+        left -= t1 - t0;
+        at = 0;
+        ++unit;
     }
 }
 
@@ -577,20 +595,25 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     a.lse = lse;
     a.acc_in = acc_in;
     a.acc_out = acc_out;
-    if (kFour && a.rows >= kTcLeastRows) {
-        if (allow_smem<accumulate_weights_tc_kernel>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
+    const int64_t units = (int64_t)c.B * c.H_kv, fit = 2 * 148;
+    const int64_t blocks = sel_idx ? n_max : (c.max_len + c.b - 1) / c.b;
+    const int64_t tiles = blocks * (c.b / kTileTokens), most = (tiles + kWarps - 1) / kWarps;
+    // few tiles (at most four a warp): a CTA works on one unit, which saves the search for its share
+    const bool few = units <= fit && units * tiles <= fit * kWarps * 4;
+    if (kFour && (!few || a.rows >= kTcLeastRows)) {
         // every CTA that fits (two an SM) once, and at least one tile a warpgroup
-        const int64_t tiles = ((int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kStripTokens) + 3) / 4;
-        const int64_t most = (tiles * c.B * c.H_kv + kTcGroups - 1) / kTcGroups;
-        dim3 grid((unsigned)(most < 1 ? 1 : most < 2 * 148 ? most : 2 * 148));
-        return launch(accumulate_weights_tc_kernel, grid, dim3(kTcThreads), kTcSmem, stream, a);
+        const int64_t wide = (blocks * (c.b / kStripTokens) + 3) / 4, groups = (wide * units + kTcGroups - 1) / kTcGroups;
+        if (allow_smem<accumulate_weights_tc_kernel>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
+        return launch(accumulate_weights_tc_kernel, dim3((unsigned)(groups < 1 ? 1 : groups < fit ? groups : fit)),
+                      dim3(kTcThreads), kTcSmem, stream, a);
     }
-    // one tile a warp at least; up to eight CTAs per SM's worth of them, so ragged lengths even out
-    const int64_t tiles = (int64_t)(sel_idx ? n_max : (c.max_len + c.b - 1) / c.b) * (c.b / kTileTokens);
-    const int64_t most = (tiles + kWarps - 1) / kWarps, want = 8 * 148 / ((int64_t)c.B * c.H_kv);
-    const int64_t x = want < 1 ? 1 : want;
-    dim3 grid((unsigned)(x < most ? x : most < 1 ? 1 : most), c.H_kv, c.B);
-    return launch(accumulate_weights_kernel<kFour>, grid, dim3(kThreads), 0, stream, a);
+    if (few) {
+        const int64_t x = fit / units < most ? fit / units : most;
+        return launch(accumulate_weights_kernel<kFour, false>, dim3((unsigned)(x < 1 ? 1 : x), c.H_kv, c.B), dim3(kThreads), 0,
+                      stream, a);
+    }
+    if constexpr (kFour) return SBA_OK;  // (taken by the tensor-memory kernel above)
+    else return launch(accumulate_weights_kernel<false, true>, dim3((unsigned)fit), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace
