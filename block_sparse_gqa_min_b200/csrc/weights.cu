@@ -304,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
 // Two CTAs of two warpgroups share an SM; every warpgroup works on tiles of its own, so one's conversion
 // and its wait for the tensor core overlap the others' exponentials.
 // ---------------------------------------------------------------------------
-constexpr int kTcLeastRows = 24;
 constexpr int kTcThreads = 256;
 constexpr int kTcGroups = kTcThreads / 128;
 constexpr int kTcChunk = 64;                     // rows of one MMA
@@ -331,6 +330,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+template <bool kFour>
 __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Args a) {
     extern __shared__ uint8_t dyn_raw[];
     uint8_t* qs = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_raw) + 1023) & ~uintptr_t(1023));
@@ -406,22 +406,26 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
             __syncthreads();  // the rows before are done with
             if (tid < kTcRows / kTcChunk) chunk_plain[tid] = 1;
             __syncthreads();
-            Keys<true> next[2];
-            int64_t from = -1;  // cache row of the strip held in `next`, and its first token
+            Keys<kFour> next[2];
+            int64_t from = -1;  // cache row of the strip in hand (four bits: held in `next`), and its first token
             int from_tok = 0;
             auto fetch = [&](int x) {
                 if ((x & 31) == 0) resolve(x + lane);
                 from = __shfl_sync(0xffffffffu, row, x & 31);
                 from_tok = __shfl_sync(0xffffffffu, tok, x & 31);
-                if (from >= 0) {
+                if (from < 0) return;
+                if (kFour) {
                     next[0].load(a.k, from, lane);
                     next[1].load(a.k, from + 16, lane);
+                } else {  // a tile of bf16 keys would take 64 registers: it waits in L2, a row a lane
+                    const uint8_t* p = a.k + (from + lane) * (kHeadDim * 2);
+                    asm volatile("prefetch.global.L2 [%0];\n\tprefetch.global.L2 [%0+128];" ::"l"(p));
                 }
             };
             if (mine > 0) fetch(0);
-            // ---- the rows, scaled to a maximum in [1, 2) each, as f16 in the B operand's layout: 16 lanes a
-            // row, lane m the 16-byte chunk m of its 128 positions (64 in each half).  Position 16p + 4i + x
-            // is channel 32i + 4p + x, the order in which the key operand is stored ----
+            // ---- the rows (for four-bit keys as f16, scaled to a maximum in [1, 2) each) in the B operand's
+            // layout: 16 lanes a row, lane m the 16-byte chunk m of its 128 positions (64 in each half).
+            // Position 16p + 4i + x is channel channel(p, i, 0) + x, the order in which the keys are stored ----
             constexpr int kStep = kTcThreads / 16, kBatch = 4;  // rows of one pass, passes whose loads go together
             const int m = tid & 15, p = m >> 1, i0 = 2 * (m & 1);
             for (int rb = tid >> 4; rb < n_pad; rb += kStep * kBatch) {
@@ -435,8 +439,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                     if (r < n_rows) {
                         const int64_t qrow = ((int64_t)s * a.M + gr / G) * a.H_q + h * G + gr % G;
                         const uint2* src = reinterpret_cast<const uint2*>(a.q + qrow * kHeadDim);
-                        x0[y] = __ldca(src + 8 * i0 + p);
-                        x1[y] = __ldca(src + 8 * (i0 + 1) + p);
+                        x0[y] = __ldca(src + Keys<kFour>::channel(p, i0, 0) / 4);
+                        x1[y] = __ldca(src + Keys<kFour>::channel(p, i0 + 1, 0) / 4);
                         lse[y] = __ldca(a.lse + qrow);
                     }
                 }
@@ -445,26 +449,31 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                     const int r = rb + y * kStep;
                     if (r >= n_pad) break;  // the same for a whole warp: n_pad is a multiple of 16
                     const uint32_t w[4] = {x0[y].x, x0[y].y, x1[y].x, x1[y].y};
-                    float mx = 0.f;
+                    uint32_t f[4] = {w[0], w[1], w[2], w[3]};
+                    float up = 1.f;
+                    if (kFour) {
+                        float mx = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
+                        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(w[e])), fabsf(bf16_hi(w[e]))));
 #pragma unroll
-                    for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    const int e2 = row_exponent(mx);
-                    const float down = pow2(-e2);
-                    uint32_t f[4];
+                        for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        const int e2 = row_exponent(mx);
+                        const float down = pow2(-e2);
+                        up = pow2(e2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+                        for (int e = 0; e < 4; ++e) f[e] = pack_f16(bf16_lo(w[e]) * down, bf16_hi(w[e]) * down);
+                    }
                     *reinterpret_cast<uint4*>(qs + (m >> 3) * (kTcRows * 128) + r * 128 + (((m & 7) ^ (r & 7)) << 4)) =
                         make_uint4(f[0], f[1], f[2], f[3]);
                     if (m == 0) {
                         // a row that attended to nothing adds nothing
                         const bool counts = lse[y] > -INFINITY || lse[y] != lse[y];
                         float* rp = reinterpret_cast<float*>(row_p + r / 2) + (r & 1);
-                        rp[0] = counts ? a.scale_log2 * pow2(e2) : 0.f;
+                        rp[0] = counts ? a.scale_log2 * up : 0.f;
                         rp[2] = counts ? -lse[y] * kLog2e : -INFINITY;
                         row_lim[r] = counts ? len - a.M + (r0 + r) / G + 1 : 0;
-                        if (!counts && r < n_rows) chunk_plain[r / kTcChunk] = 0;
+                        // (a padding row times an infinite bf16 key is a NaN: masked like a row without an lse)
+                        if (!counts && (r < n_rows || !kFour)) chunk_plain[r / kTcChunk] = 0;
                     }
                 }
             }
@@ -474,8 +483,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
             const float* acc_from = r0 ? a.acc_out : a.acc_in;
             const uint64_t db = tc::smem_desc(tc::uniform(smem_u32(qs)), 1024);
             for (int x = 0; x < mine; ++x) {
-                // ---- keys of `next` to the A operand (a strip that is not there leaves what `next` held: its
-                // tokens are not written) ----
+                // ---- the keys to the A operand (a strip that is not there leaves what `next` held: its tokens
+                // are not written) ----
+                if (!kFour && from >= 0) {
+                    next[0].load(a.k, from, lane);
+                    next[1].load(a.k, from + 16, lane);
+                }
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t f[8][4], v[32];
@@ -503,7 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
                     if (issuer && __all_sync(0xffffffffu, alive)) {
                         tc::fence_after();
-                        const uint32_t id = tc::idesc(128, n, false), step = (uint32_t)c0 * 128 >> 4;
+                        const uint32_t id = tc::idesc(128, n, !kFour), step = (uint32_t)c0 * 128 >> 4;
                         if (tc::elect()) {
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
@@ -600,11 +613,17 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     const int64_t tiles = blocks * (c.b / kTileTokens), most = (tiles + kWarps - 1) / kWarps;
     // few tiles (at most four a warp): a CTA works on one unit, which saves the search for its share
     const bool few = units <= fit && units * tiles <= fit * kWarps * 4;
-    if (kFour && (!few || a.rows >= kTcLeastRows)) {
+    // Rows from which the tensor-memory kernel is taken, measured on both sides (8 KV heads; us with mma.sync
+    // against tcgen05).  Four bits, 393K tokens: 4 rows 116 against 71, 64 rows 270 against 104.  bf16, 393K
+    // tokens: 20 rows 162 (the tcgen05 kernel at 24 rows: 164), 32 rows 186 against 161, 64 rows 271 against 183.  A short launch
+    // pays for its longer start: four bits, 16K tokens: 16 rows 8.3 against 8.2, 32 rows 10.7 against 9.2; 4K
+    // tokens: 32 rows 5.9 against 6.4, 64 rows 8.2 against 7.6; bf16, 16K tokens: 32 rows 11.7 against 13.2, 64 rows 16.2 against 15.2.
+    const int least = few ? (kFour ? 24 : 64) : (kFour ? 1 : 24);
+    if (a.rows >= least) {
         // every CTA that fits (two an SM) once, and at least one tile a warpgroup
         const int64_t wide = (blocks * (c.b / kStripTokens) + 3) / 4, groups = (wide * units + kTcGroups - 1) / kTcGroups;
-        if (allow_smem<accumulate_weights_tc_kernel>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
-        return launch(accumulate_weights_tc_kernel, dim3((unsigned)(groups < 1 ? 1 : groups < fit ? groups : fit)),
+        if (allow_smem<accumulate_weights_tc_kernel<kFour>>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
+        return launch(accumulate_weights_tc_kernel<kFour>, dim3((unsigned)(groups < 1 ? 1 : groups < fit ? groups : fit)),
                       dim3(kTcThreads), kTcSmem, stream, a);
     }
     if (few) {

@@ -71,6 +71,10 @@ WEIGHTS = [
     (True, 64, [900, 5], 1, 16, True, 20, 0, False),     # 320 rows
     (True, 64, [3000, 70], 2, 6, True, 4, 9, False),     # 24 rows over an odd number of blocks
     (True, 128, [4000], 1, 11, False, 7, 5, False),      # 77 rows
+    (False, 64, [3000, 70], 2, 6, True, 4, 9, False),
+    (False, 128, [2222, 64], 1, 11, True, 7, 0, False),
+    (False, 64, [40000, 100, 2500], 8, 2, True, 1, 0, False),   # long: shares that span sequences
+    (True, 64, [40000, 100, 2500], 8, 2, True, 1, 0, False),
 ]
 
 
