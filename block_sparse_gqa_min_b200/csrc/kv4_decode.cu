@@ -36,8 +36,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
-constexpr int kRing = kWarps * kStages * kStripBytes;
+constexpr int kFlush = 8;  // strips after which fp32 outputs move their sums out of the MMA accumulators
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMostParts = 128;           // of one unit: the merge of more would take longer than they save
@@ -89,6 +88,17 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// An MMA drops what does not fit its accumulator instead of rounding it, so a long chain of them drifts
+// (fp32 outputs over 98K strips: 1.3e-6 off, and 7e-7 with the sums below; the plain fp32 form 4e-7).  For fp32 outputs a lane
+// therefore adds its accumulators to sums of its own in shared memory every kFlush strips.
+template <int NH, bool kSplitP>
+struct Layout {
+    static constexpr int kStages = kSplitP ? 2 : 3;
+    static constexpr int kWarpRing = kStages * kStripBytes;
+    static constexpr int kSums = kSplitP ? NH * 32 * 32 * 4 : 0;  // per warp: [32 NH values][32 lanes]
+    static constexpr int kBytes = kWarps * (kWarpRing + kSums);
+};
+
 template <int NH>
 struct State {
     float o[NH][8][4];  // O^T: [row tile][channel pair mt]: channels 16(lane/4) + 2mt (c0, c1) and + 1 (c2, c3) of
@@ -102,7 +112,7 @@ struct State {
 
 template <int NH, bool kSplitP>
 __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)[NH][8][2], uint8_t* strip, int tok0,
-                                             int valid, bool partial, int first_hidden, int lane) {
+                                             int valid, bool partial, int first_hidden, float* sums, int lane) {
     const int tr = lane >> 2, i = lane & 3;
     // partial: some row does not see some token of the strip
     if (partial && valid < kStripTokens) {
@@ -213,6 +223,10 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
                     for (int mt = 0; mt < 8; ++mt) {
                         st.o[nh][mt][x] *= alpha;
                         st.o[nh][mt][2 + x] *= alpha;
+                        if (kSplitP) {  // (not in use, and not read, where the warp has fewer than kFlush strips)
+                            sums[((nh * 8 + mt) * 4 + x) * 32] *= alpha;
+                            sums[((nh * 8 + mt) * 4 + 2 + x) * 32] *= alpha;
+                        }
                     }
                 }
             }
@@ -300,11 +314,28 @@ __device__ __forceinline__ void add_weighted(float4& v, float f, float4 o) {
     v.w = fmaf(f, o.w, v.w);
 }
 
+// This lane's accumulators into its sums (or, to end with, its sums into the accumulators).
+template <int NH>
+__device__ __forceinline__ void move_sums(State<NH>& st, float* sums, bool back) {
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float& s = sums[((nh * 8 + mt) * 4 + x) * 32];
+                const float all = s + st.o[nh][mt][x];
+                st.o[nh][mt][x] = back ? all : 0.f;
+                if (!back) s = all;
+            }
+}
+
 // kShared: a CTA takes an equal share of all units' strips, which may span several units; else the grid
 // is (CTAs a unit, KV heads x row groups, sequences) and a CTA works on one unit.
 template <int NH, bool kSplitP, bool kShared>
 __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(Args a) {
-    constexpr int R = 8 * NH;
+    using L = Layout<NH, kSplitP>;
+    constexpr int R = 8 * NH, kStages = L::kStages;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ int2 info[kWarps][kStages];  // first token of the strip; valid tokens in it, negative if some row does not see all 32
@@ -343,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             return (int)min(n, (int64_t)gridDim.x);
         });
     }
-    uint8_t* my_ring = ring + warp * (kStages * kStripBytes);
+    uint8_t* my_ring = ring + warp * L::kWarpRing;
+    float* sums = reinterpret_cast<float*>(ring + kWarps * L::kWarpRing + warp * L::kSums) + lane;
     int seq = 0;        // strips this warp has been through (their stages and phases)
     bool alive = true;  // no wait of this warp has run out
 
@@ -465,6 +497,9 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
         }
 
         const int first_hidden = len - a.M + 1;  // the first token that some row does not see
+        if (kSplitP && mine >= kFlush)
+#pragma unroll
+            for (int e = 0; e < NH * 32; ++e) sums[e * 32] = 0.f;
         for (int x = 0; x < mine; ++x) {
             const int stage = (seq + x) % kStages;
             if (!mbar_wait(&full[warp][stage], ((seq + x) / kStages) & 1, a.status)) {
@@ -481,12 +516,14 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             }
             const int2 inf = info[warp][stage];
             if (inf.y != 0)
-                attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, abs(inf.y), inf.y < 0, first_hidden, lane);
+                attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, abs(inf.y), inf.y < 0, first_hidden, sums, lane);
+            if (kSplitP && x % kFlush == kFlush - 1) move_sums(st, sums, false);
             __syncwarp();
             if (x + kStages < mine) issue(x + kStages);
         }
 
         seq += mine;
+        if (kSplitP && mine >= kFlush) move_sums(st, sums, true);
 
         // ---- merge the warps: each leaves its rows in its own ring ----
         float* mo = reinterpret_cast<float*>(my_ring);
@@ -526,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
                 const float fw = __shfl_sync(0xffffffffu, f, w);
                 if (fw != 0.f)  // (a warp without strips left its ring as it was)
                     add_weighted(acc[x], fw, *reinterpret_cast<const float4*>(
-                        reinterpret_cast<const float*>(ring + w * (kStages * kStripBytes)) + r * kRowStride + 4 * lane));
+                        reinterpret_cast<const float*>(ring + w * L::kWarpRing) + r * kRowStride + 4 * lane));
             }
         }
         if (s1 - s0 < T) {
@@ -671,9 +708,9 @@ Plan plan_of(const sba_cache4& c, int M, int n_max) {
 
 template <int NH, bool kSplitP, bool kShared>
 int launch_one(const Args& a, const Plan& p, cudaStream_t stream) {
-    if (allow_smem<decode_kv4_kernel<NH, kSplitP, kShared>>(kRing) != SBA_OK) return SBA_ERR_CUDA;
+    if (allow_smem<decode_kv4_kernel<NH, kSplitP, kShared>>(Layout<NH, kSplitP>::kBytes) != SBA_OK) return SBA_ERR_CUDA;
     const dim3 grid = kShared ? dim3(p.ctas) : dim3(p.parts, a.H_kv * a.row_groups, a.B);
-    return launch(decode_kv4_kernel<NH, kSplitP, kShared>, grid, dim3(kThreads), kRing, stream, a);
+    return launch(decode_kv4_kernel<NH, kSplitP, kShared>, grid, dim3(kThreads), Layout<NH, kSplitP>::kBytes, stream, a);
 }
 
 template <int NH>
