@@ -59,7 +59,7 @@ struct Args {
     void* out;
     int out_bf16;
     float* lse_out;
-    uint32_t* counters;  // [unit], a unit being one (sequence, KV head, row group)
+    uint32_t* counters;  // parts that have come, by unit ((sequence, KV head, row group)) or, equal shares, by a unit's first CTA
     float* part_ml;      // [part][R][2]; parts: [unit][CTA of it], or (equal shares) [CTA][its first unit's, its last's]
     float* part_o;       // [part][R][128], unnormalised
 };
@@ -584,12 +584,13 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             }
             __threadfence();
             __syncthreads();
-            if (tid == 0) last = atomicAdd(a.counters + unit, 1u) == (uint32_t)parts - 1;
+            uint32_t* counter = a.counters + (kShared ? c0 : unit);  // (two shared units have different first CTAs)
+            if (tid == 0) last = atomicAdd(counter, 1u) == (uint32_t)parts - 1;
             __syncthreads();
             write = last;
             if (write) {
                 __threadfence();
-                if (tid == 0) a.counters[unit] = 0u;  // ready for the next call
+                if (tid == 0) *counter = 0u;  // ready for the next call
                 // part y's rows; a part is its CTA's first unit's, unless the CTA began before the unit (only the first can)
                 constexpr int kStep = kShared ? 2 * R : R;
                 int64_t row0 = (int64_t)unit * gridDim.x * R, part0 = row0;
@@ -672,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
 }
 
 constexpr int kRefSMs = 148;
+constexpr int kCounters = 512;  // 2 * kRefSMs at most are in use
 
 struct Plan {
     int NH, row_groups, parts, ctas;
@@ -699,7 +701,7 @@ Plan plan_of(const sba_cache4& c, int M, int n_max) {
         if (units * strips < fit * kWarps) p.ctas = (int)((units * strips + kWarps - 1) / kWarps);
     }
     const size_t R = 8 * p.NH;
-    p.ml = ((size_t)units * 4 + 255) / 256 * 256;
+    p.ml = kCounters * 4;  // at the same place whatever the shape: one workspace serves all
     const size_t parts = (size_t)p.ctas * (p.parts ? 1 : 2);
     p.o = p.ml + parts * R * 2 * 4;
     p.total = p.o + parts * R * kHeadDim * 4;

@@ -468,11 +468,10 @@ int sba_score_select_kv4(const sba_cache4 *c, const void *q, int32_t M, const sb
  * out       device [B][M][H_q][d] in out_dtype (SBA_OUT_F32 or SBA_OUT_BF16), 16-byte aligned;
  *           0 for a row that sees no token.
  * lse_out   device fp32 [B][M][H_q] or NULL: log sum exp of the row's logits, -inf if it sees none.
- * ws        device workspace of at least sba_decode_kv4_workspace_size() bytes (same cache shape, M and
- *           n_max), 16-byte aligned, ZERO-FILLED before its first use; every completed call leaves its
- *           counters at zero again.  Calls that share a workspace must not run concurrently, and one
- *           workspace serves one (cache shape, M, n_max): other shapes lay it out differently, so zero
- *           it again in between. */
+ * ws        device workspace of at least sba_decode_kv4_workspace_size() bytes, 16-byte aligned,
+ *           ZERO-FILLED before its first use; every completed call leaves its counters at zero again, so
+ *           calls of any shapes may use it one after another.  Calls that share a workspace must not run
+ *           concurrently (a graph that holds calls and eager calls beside it: a workspace each). */
 size_t sba_decode_kv4_workspace_size(const sba_cache4 *c, int32_t M, int32_t n_max);
 int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t *sel_idx, const int32_t *sel_cnt,
                    int32_t n_max, float softmax_scale, void *out, int32_t out_dtype, float *lse_out, void *ws,
@@ -487,8 +486,9 @@ int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t 
  *               is -inf adds nothing.
  * gate_bias     as sba_sparse_decode (fp32 [B][H_q][n_max]), or NULL; needs a selection and M = 1.
  * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); may be the same.
- * A selection lists every block once, ascending (SBA_DEV_BAD_SELECTION otherwise, and the block is
- * skipped).  No atomics: the same inputs give the same bits. */
+ * A selection lists every block once, ascending; an entry that is not larger than the one before it is
+ * skipped and reports SBA_DEV_BAD_SELECTION (what a list that still names a block twice adds to that
+ * block is not defined).  No atomics: the same inputs give the same bits. */
 int sba_accumulate_weights(const sba_cache *c, const void *q, int32_t M, const int32_t *sel_idx,
                            const int32_t *sel_cnt, const float *gate_bias, int32_t n_max, float softmax_scale,
                            const float *lse, const float *acc_in, float *acc_out, void *stream);

@@ -369,6 +369,38 @@ def test_decode_in_a_graph_and_on_another_stream():
         check_decode(c, kv.numpy(), lay, q2, None, got, l2, 64, 4, True)
 
 
+def test_decode_one_workspace_for_all_shapes():
+    """A workspace of the largest size, zeroed once, serves calls of other shapes in any order: short and long
+    caches (one unit a CTA; shares that span units), one and several tokens, selections."""
+    cases = [decode_case(64, [700, 90], 2, 4, True, 1, 0, True, seed=21),
+             decode_case(64, [40000, 333, 0, 9000], 2, 2, True, 1, 0, True, seed=22),
+             decode_case(128, [300], 1, 8, False, 4, 0, True, seed=23),
+             decode_case(64, [2000, 64], 2, 4, True, 1, 9, True, seed=24)]
+    sizes = [sba.sba_decode_kv4_workspace_size(c, q.shape[1], 0 if sel is None else 9) for _, _, q, c, sel in cases]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device=DEV)
+    own = [run_decode(c, q, sel, True)[:2] for _, _, q, c, sel in cases]
+    for i in (0, 1, 2, 3, 1, 0, 3, 2, 2, 1):
+        lay, kv, q, c, sel = cases[i]
+        out, lse, _ = run_decode(c, q, sel, True, ws)
+        assert torch.equal(out, own[i][0]) and torch.equal(lse, own[i][1])
+    lay, kv, q, c, sel = cases[1]
+    check_decode(c, kv.numpy(), lay, q, sel, *own[1], 64, 2, True)
+    lay, kv, q, c, sel = cases[2]
+    check_decode(c, kv.numpy(), lay, q, sel, *own[2], 128, 8, True)
+
+
+@pytest.mark.parametrize("lens,H,G,M,f32", [([50000, 20000, 7, 33000], 4, 4, 1, True), ([60000], 2, 8, 2, False),
+                                            ([9000] * 12, 4, 2, 1, True)])
+def test_decode_long_launches(lens, H, G, M, f32):
+    """Launches whose CTAs take equal shares of all sequences: units split over many CTAs, units within one,
+    several units in one CTA."""
+    lay, kv, q, c, sel = decode_case(64, lens, H, G, True, M, 0, f32, seed=31)
+    out, lse, ws = run_decode(c, q, sel, f32)
+    check_decode(c, kv.numpy(), lay, q, sel, out, lse, 64, G, f32)
+    again = run_decode(c, q, sel, f32, ws)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and int(c.status.item()) == 0
+
+
 def test_decode_pages_past_four_gigabytes():
     """Pages whose byte offsets do not fit 32 bits."""
     b, H, G = 128, 4, 4
