@@ -245,6 +245,66 @@ def test_evict_matches_oracle(four, b, lens, H, paged, n_keep, n_sink, n_recent,
         assert np.array_equal(f64(dst.k), want_k) and np.array_equal(f64(dst.v), want_v)
 
 
+def test_evict_slices_longer_than_shared_memory():
+    """More heads than the GPU holds clusters, each with more tokens than one CTA keeps in shared memory."""
+    b, H, n, keep = 64, 80, 60000, 700
+    lay, dlay = layout([n], b, False, 1, slack=0), layout([keep], b, False, 2, slack=0)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv = torch.randint(0, 256, (lay.pages, H, b // 32, 4608), generator=g, dtype=torch.uint8, device=DEV)
+    kv[..., 4096:] %= 227
+    src, dst = cache4(lay, kv, H_q=H, desc=False), cache4(dlay, torch.zeros((dlay.pages, H, b // 32, 4608), dtype=torch.uint8), H)
+    acc = torch.round(torch.exp(2 * torch.randn((lay.pages, H, b), generator=g, device=DEV)))
+    new_lens, kept = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros((1, H, keep), dtype=torch.int32, device=DEV)
+    sba.sba_evict_kv4(src, acc, sba.evict_params(keep, 5, 40), dst, new_lens, kept)
+    assert new_lens.tolist() == [keep] and int(src.status.item()) == 0
+    a, got = acc.cpu().numpy(), kept.cpu().numpy()
+    for h in (0, 41, 79):
+        assert np.array_equal(got[0, h], SC.keep(SC.gather(a, None, 0, lay.max_blocks, h, n), keep, 5, 40))
+        t = torch.from_numpy(got[0, h]).long().to(DEV)
+        rows = src.kv[t // b, h, (t % b) // 32, :2048].reshape(keep, 32, 64)[torch.arange(keep), t % 32]
+        i = torch.arange(keep, device=DEV)
+        moved = dst.kv[i // b, h, (i % b) // 32, :2048].reshape(keep, 32, 64)[torch.arange(keep), i % 32]
+        assert torch.equal(rows, moved)
+
+
+def test_weights_past_four_gigabytes_and_understated_selection():
+    """Key pages whose byte offsets do not fit 32 bits (bf16 and four bits, few rows and many), and selections
+    shorter than their row."""
+    b, H, G = 128, 4, 8
+    for four, M in ((False, 1), (False, 9), (True, 1), (True, 9)):
+        lay = layout([700], b, True, 1)
+        per = H * b // 32 * 4608 if four else H * b * 256
+        pages = (5 << 30) // per
+        lay.table[0, :6] = np.arange(pages - 9, pages - 3)[::-1]
+        k = rand_bf16((6, H, b, 128), 3)
+        small = layout([700], b, False, 1, slack=0)
+        if four:
+            big = torch.zeros((pages, H, b // 32, 4608), dtype=torch.uint8, device=DEV)
+            rows = packed(k, k)
+            big[torch.from_numpy(lay.table[0, :6]).long().to(DEV)] = rows.to(DEV)
+            K = SC.unpack_tile(rows.numpy())[0]
+            lay.pages = pages
+            c = cache4(lay, big, H_q=H * G, desc=False)
+        else:
+            big = torch.zeros((pages, H, b, 128), dtype=torch.bfloat16, device=DEV)
+            big[torch.from_numpy(lay.table[0, :6]).long().to(DEV)] = k.to(DEV)
+            K = f64(k)
+            lay.pages = pages
+            c = cache16(lay, big, big, H_q=H * G, desc=False)
+        q = rand_bf16((1, M, H * G, 128), 5, 0)
+        lse = torch.full((1, M, H * G), 5.0)
+        idx = torch.tensor([[[0, 2, 5, 900]] * H], dtype=torch.int32, device=DEV)     # the last entry does not count
+        cnt = torch.full((1, H), 3, dtype=torch.int32, device=DEV)
+        acc = torch.zeros((pages, H, b), device=DEV)
+        call = sba.sba_accumulate_weights_kv4 if four else sba.sba_accumulate_weights
+        call(c, q.to(DEV), lse.to(DEV), SCALE, acc, acc, sel_idx=idx, sel_cnt=cnt)
+        assert int(c.status.item()) == 0
+        got = acc[torch.from_numpy(lay.table[0, :6]).long().to(DEV)].cpu()
+        sel = (np.array([[[0, 2, 5]] * H]), np.full((1, H), 3))
+        check_weights(small, b, G, K, q, lse, sel, None, torch.zeros(got.shape), got, np.zeros(got.shape))
+        del big, acc, c
+
+
 def test_evict_bad_pages_are_skipped_and_reported():
     b, H = 64, 1
     lay, dlay = layout([640], b, True, 1), layout([128], b, True, 2, slack=0)
