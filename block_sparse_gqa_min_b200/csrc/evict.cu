@@ -108,13 +108,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     uint32_t* own = dyn + (lane & (kCopies - 1)) * kCopyStride;
     // (asynchronous copies: what little L1 the keys leave could not hold this many loads in flight)
     const int held = min(nq, cap / 4);
-    for (int i = tid; i < held; i += kSelThreads) {
-        const int cell = cell_of(i);
-        if (cell >= 0) {
-            cp_async_16(keys + 4 * i, a.acc + cell);
-        } else {
-            report(a.status, SBA_DEV_BAD_PAGE);
-            *reinterpret_cast<float4*>(keys + 4 * i) = weights_of(-1);
+    constexpr int kLoads = 8;  // page lookups in flight
+    for (int i0 = tid; i0 < held; i0 += kLoads * kSelThreads) {
+        int cell[kLoads];
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) cell[x] = i0 + x * kSelThreads < held ? cell_of(i0 + x * kSelThreads) : 0;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            const int i = i0 + x * kSelThreads;
+            if (i >= held) break;
+            if (cell[x] >= 0) {
+                cp_async_16(keys + 4 * i, a.acc + cell[x]);
+            } else {
+                report(a.status, SBA_DEV_BAD_PAGE);
+                *reinterpret_cast<float4*>(keys + 4 * i) = weights_of(-1);
+            }
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // this thread's own, and it reads no other's
@@ -194,12 +202,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     // but the threads' totals ----
     const int per = ((nq + kSelThreads - 1) / kSelThreads) | 1;
     const int i0 = min(nq, tid * per), i1 = min(nq, i0 + per);
+    uint64_t above = 0, at = 0;  // its tokens above and at the threshold, a bit each, where they fit
     uint32_t gt = 0, eq = 0;
 #pragma unroll 4
     for (int i = i0; i < i1; ++i) {
         const uint4 r = quad(i);
-        gt += (r.x > T) + (r.y > T) + (r.z > T) + (r.w > T);
-        eq += (r.x == T) + (r.y == T) + (r.z == T) + (r.w == T);
+        const uint32_t bg = (r.x > T) | (r.y > T) << 1 | (r.z > T) << 2 | (r.w > T) << 3;
+        const uint32_t be = (r.x == T) | (r.y == T) << 1 | (r.z == T) << 2 | (r.w == T) << 3;
+        above |= (uint64_t)bg << (4 * (i - i0) & 63);
+        at |= (uint64_t)be << (4 * (i - i0) & 63);
+        gt += __popc(bg);
+        eq += __popc(be);
     }
     uint32_t g = gt, e = eq;  // the tokens of this thread and those before it: warp, CTA, cluster
 #pragma unroll
@@ -224,9 +237,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     }
     g += __reduce_add_sync(0xffffffffu, n_c.x);
     e += __reduce_add_sync(0xffffffffu, n_c.y);
-    // only now: CTAs of the next kernel that come earlier take the place of a large cluster's
     pdl_trigger();
-    if (gt + eq > 0) {
+    if (per <= 16) {
+        for (uint64_t rest = above | at; rest; rest &= rest - 1) {
+            const int bit = __ffsll((long long)rest) - 1;
+            const bool is_at = at >> bit & 1;
+            if (!is_at || e < left) kept[sink + g + min(e, left)] = 4 * (q0 + i0) + bit;
+            g += !is_at;
+            e += is_at;
+        }
+    } else if (gt + eq > 0) {
         for (int i = i0; i < i1; ++i) {
             const uint4 r = quad(i);
             const uint32_t v[4] = {r.x, r.y, r.z, r.w};

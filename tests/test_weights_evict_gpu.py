@@ -247,7 +247,7 @@ def test_evict_matches_oracle(four, b, lens, H, paged, n_keep, n_sink, n_recent,
 
 def test_evict_slices_longer_than_shared_memory():
     """More heads than the GPU holds clusters, each with more tokens than one CTA keeps in shared memory."""
-    b, H, n, keep = 64, 80, 60000, 700
+    b, H, n, keep = 64, 80, 70000, 700
     lay, dlay = layout([n], b, False, 1, slack=0), layout([keep], b, False, 2, slack=0)
     g = torch.Generator(device="cuda").manual_seed(3)
     kv = torch.randint(0, 256, (lay.pages, H, b // 32, 4608), generator=g, dtype=torch.uint8, device=DEV)
