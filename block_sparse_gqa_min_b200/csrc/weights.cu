@@ -10,7 +10,9 @@
 // read straight from global memory into operand registers, with the next tile's keys in flight; the
 // query rows are the columns, 8 at a time, kept in shared memory as operand fragments.  The channels
 // of an MMA step are permuted alike in both so that every lane's key reads are 16 bytes.
-// With few rows the bytes of K bound it (one read of 256 or 72 bytes a token); with many, the MMAs.
+// With few rows the bytes of K bound it: bf16, 8 sequences of 32-64K, 8 KV heads, 4 rows: 135 us, 94% of the
+// copy bandwidth; a gated step's 32 blocks of 64 tokens: 4.5 us.  Many rows, and long four-bit launches, go to
+// the second kernel below.
 #include <math.h>
 
 #include <type_traits>
@@ -300,7 +302,10 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
 // a warp brings its strip of 32 tokens from codes to f16 and stores it as the A operand in tensor
 // memory, one thread issues the eight steps of 16 channels against the rows in shared memory, and every
 // thread reads back the 64 logits of ONE token, so the sum over the rows is in its own registers (no
-// shuffle, no shared memory).  What bounds it is the 16 exponentials a cycle of an SM.
+// shuffle, no shared memory).  What bounds it is the 16 exponentials a cycle of an SM: 64 rows over 393K tokens
+// and 8 KV heads would take 45 us at that rate and take 103 (four bits; 183 in bf16, where the keys alone
+// take 127): the unit is 47% busy, since a tile's steps (codes to f16 0.4 us, products 0.3, exponentials 0.9)
+// follow one another and tensor memory has room for four tiles an SM.
 // Two CTAs of two warpgroups share an SM; every warpgroup works on tiles of its own, so one's conversion
 // and its wait for the tensor core overlap the others' exponentials.
 // ---------------------------------------------------------------------------
@@ -613,11 +618,12 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     const int64_t tiles = blocks * (c.b / kTileTokens), most = (tiles + kWarps - 1) / kWarps;
     // few tiles (at most four a warp): a CTA works on one unit, which saves the search for its share
     const bool few = units <= fit && units * tiles <= fit * kWarps * 4;
-    // Rows from which the tensor-memory kernel is taken, measured on both sides (8 KV heads; us with mma.sync
-    // against tcgen05).  Four bits, 393K tokens: 4 rows 116 against 71, 64 rows 270 against 104.  bf16, 393K
-    // tokens: 20 rows 162 (the tcgen05 kernel at 24 rows: 164), 32 rows 186 against 161, 64 rows 271 against 183.  A short launch
-    // pays for its longer start: four bits, 16K tokens: 16 rows 8.3 against 8.2, 32 rows 10.7 against 9.2; 4K
-    // tokens: 32 rows 5.9 against 6.4, 64 rows 8.2 against 7.6; bf16, 16K tokens: 32 rows 11.7 against 13.2, 64 rows 16.2 against 15.2.
+    // Rows from which the tensor-memory kernel is taken, measured on both sides with 8 KV heads (us, mma.sync
+    // against tcgen05).  Long launches: four bits, 393K tokens: 4 rows 116 against 71, 64 rows 270 against 104;
+    // bf16: 20 rows 162 against 164 (at 24), 32 rows 186 against 161, 64 rows 271 against 183.  A short launch
+    // pays for the longer start: four bits, 16K tokens: 16 rows 8.3 against 8.2, 32 rows 10.7 against 9.2; 4K
+    // tokens: 32 rows 5.9 against 6.4, 64 rows 8.2 against 7.6; bf16, 16K tokens: 32 rows 11.7 against 13.2,
+    // 64 rows 16.2 against 15.2.
     const int least = few ? (kFour ? 24 : 64) : (kFour ? 1 : 24);
     if (a.rows >= least) {
         // every CTA that fits (two an SM) once, and at least one tile a warpgroup
