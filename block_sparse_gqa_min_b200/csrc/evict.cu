@@ -385,24 +385,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(MoveArgs a) {
 // Four-bit cache: 8 lanes move a row, four for the key codes and four for the value codes (16 bytes
 // each), every lane also the two scales of its own 32 channels.  For the descriptor the value lanes
 // take the upper half of a key lane's channels: 16 channels a lane keep the registers few, so that
-// eight CTAs share an SM (the kernel waits for its three dependent loads, not for bandwidth).
+// many CTAs share an SM (the kernel waits for its dependent loads, not for bandwidth); the threads'
+// minima and maxima meet in shared memory.
+constexpr int kMove4Threads = 128;
 template <int kBlk>
-__global__ void __launch_bounds__(kMoveThreads, kBlk == 64 ? 8 : 6) evict_move_kv4_kernel(MoveArgs a) {
-    constexpr int kIter = kBlk / 32;
+__global__ void __launch_bounds__(kMove4Threads, kBlk == 64 ? 12 : 8) evict_move_kv4_kernel(MoveArgs a) {
+    constexpr int kRowsAt = kMove4Threads / 8, kIter = kBlk / kRowsAt;
     __shared__ int64_t src[kBlk];
-    __shared__ uint32_t red[2][kMoveThreads / 32][64];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = tid & 7, r = tid >> 3;
+    __shared__ __half2 red[2][64][kRowsAt + 1];
+    const int tid = threadIdx.x, lane = tid & 31, g = tid & 7, r = tid >> 3;
     pdl_wait();
     pdl_trigger();
     int64_t page = -1;
     if (source_rows<kBlk>(a, src, page) == 0) return;
     const int codes_at = (g < 4 ? 0 : kStripV) + (g & 3) * 16, scales_at = (g < 4 ? kStripKS : kStripVS) + (g & 3) * 2;
-    uint8_t* tile = a.k_dst + (page * a.H_kv + blockIdx.y) * (int64_t)(kIter * kStripBytes);
+    uint8_t* tile = a.k_dst + (page * a.H_kv + blockIdx.y) * (int64_t)(kBlk / kStripTokens * kStripBytes);
     uint4 code[kIter];
     uint32_t sc[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const int64_t from = src[r + 32 * i];
+        const int64_t from = src[r + kRowsAt * i];
         code[i] = make_uint4(0u, 0u, 0u, 0u);
         sc[i] = 0;
         if (from >= 0) {
@@ -419,11 +421,12 @@ __global__ void __launch_bounds__(kMoveThreads, kBlk == 64 ? 8 : 6) evict_move_k
     }
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
-        const bool real = src[r + 32 * i] >= 0;
+        const int row = r + kRowsAt * i;
+        const bool real = src[row] >= 0;
         if (real) {
-            uint8_t* strip = tile + i * kStripBytes;
-            *reinterpret_cast<uint4*>(strip + r * 64 + codes_at) = code[i];
-            *reinterpret_cast<uint16_t*>(strip + r * 8 + scales_at) = (uint16_t)sc[i];
+            uint8_t* strip = tile + (row >> 5) * kStripBytes;
+            *reinterpret_cast<uint4*>(strip + (row & 31) * 64 + codes_at) = code[i];
+            *reinterpret_cast<uint16_t*>(strip + (row & 31) * 8 + scales_at) = (uint16_t)sc[i];
         }
         if (a.desc) {  // channels 32(g % 4) + 16(g / 4) ..: the key lane's words x, y or z, w
             const uint32_t z = __shfl_sync(0xffffffffu, code[i].z, lane & ~4), w = __shfl_sync(0xffffffffu, code[i].w, lane & ~4);
@@ -431,39 +434,30 @@ __global__ void __launch_bounds__(kMoveThreads, kBlk == 64 ? 8 : 6) evict_move_k
             uint32_t v[8];
             codes_to_f16(g < 4 ? code[i].x : z, v[0], v[1], v[2], v[3]);
             codes_to_f16(g < 4 ? code[i].y : w, v[4], v[5], v[6], v[7]);
-            const uint32_t f = scale_f16x2(g < 4 ? ks & 0xffu : ks >> 8);
+            // a row that is not there counts as a NaN, which minimum and maximum pass over
+            const uint32_t f = scale_f16x2(!real ? kScaleNaN : g < 4 ? ks & 0xffu : ks >> 8);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t y = mul_f16x2(v[e], f);
-                if (real) {
-                    mn[e] = __hmin2(mn[e], *reinterpret_cast<const __half2*>(&y));
-                    mx[e] = __hmax2(mx[e], *reinterpret_cast<const __half2*>(&y));
-                }
+                mn[e] = __hmin2(mn[e], *reinterpret_cast<const __half2*>(&y));
+                mx[e] = __hmax2(mx[e], *reinterpret_cast<const __half2*>(&y));
             }
         }
     }
     if (!a.desc) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-#pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-            mn[e] = __hmin2(mn[e], __shfl_xor_sync(0xffffffffu, mn[e], o));
-            mx[e] = __hmax2(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
-        }
-        if (lane < 8) {
-            const int pair = (g & 3) * 16 + (g >> 2) * 8 + e;
-            red[0][warp][pair] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&mn[e]));
-            red[1][warp][pair] = f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&mx[e]));
-        }
+        const int pair = (g & 3) * 16 + (g >> 2) * 8 + e;
+        red[0][pair][r] = mn[e];
+        red[1][pair][r] = mx[e];
     }
     __syncthreads();
-    if (tid < 128) {
-        const int which = tid >> 6, pair = tid & 63;
-        uint32_t v = red[which][0][pair];
+    const int which = tid >> 6, pair = tid & 63;
+    __half2 v = red[which][pair][0];
 #pragma unroll
-        for (int w = 1; w < kMoveThreads / 32; ++w) v = which ? max2(v, red[which][w][pair]) : min2(v, red[which][w][pair]);
-        reinterpret_cast<uint32_t*>(a.desc)[((page * a.H_kv + blockIdx.y) * 2 + which) * 64 + pair] = v;
-    }
+    for (int i = 1; i < kRowsAt; ++i) v = which ? __hmax2(v, red[which][pair][i]) : __hmin2(v, red[which][pair][i]);
+    reinterpret_cast<uint32_t*>(a.desc)[((page * a.H_kv + blockIdx.y) * 2 + which) * 64 + pair] =
+        f16x2_to_bf16x2(*reinterpret_cast<const uint32_t*>(&v));
 }
 
 cudaLaunchConfig_t select_config(int C, int H_kv, int B, int smem, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -541,8 +535,8 @@ int launch_select(const Cache& src, const float* acc, const sba_evict_params& p,
 
 // In plain stream order: launched early, its CTAs waited on the SMs that the selection left idle, and
 // evict_512k took 71 us instead of 66.
-int launch_move(void (*kernel)(MoveArgs), dim3 grid, const MoveArgs& m, cudaStream_t stream) {
-    kernel<<<grid, kMoveThreads, 0, stream>>>(m);
+int launch_move(void (*kernel)(MoveArgs), dim3 grid, int threads, const MoveArgs& m, cudaStream_t stream) {
+    kernel<<<grid, threads, 0, stream>>>(m);
     return SBA_OK;  // the caller looks at cudaGetLastError
 }
 
@@ -580,7 +574,7 @@ int launch_evict(const sba_cache& src, const float* acc, const sba_evict_params&
     m.k_dst = static_cast<uint8_t*>(dst.k);
     m.v_dst = static_cast<uint8_t*>(dst.v);
     dim3 grid((p.n_keep + src.b - 1) / src.b, src.H_kv, src.B);
-    return launch_move(src.b == 64 ? evict_move_kernel<64> : evict_move_kernel<128>, grid, m, stream);
+    return launch_move(src.b == 64 ? evict_move_kernel<64> : evict_move_kernel<128>, grid, kMoveThreads, m, stream);
 }
 
 int launch_evict_kv4(const sba_cache4& src, const float* acc, const sba_evict_params& p, const sba_cache4& dst,
@@ -591,7 +585,8 @@ int launch_evict_kv4(const sba_cache4& src, const float* acc, const sba_evict_pa
     m.k_src = static_cast<const uint8_t*>(src.kv);
     m.k_dst = static_cast<uint8_t*>(dst.kv);
     dim3 grid((p.n_keep + src.b - 1) / src.b, src.H_kv, src.B);
-    return launch_move(src.b == 64 ? evict_move_kv4_kernel<64> : evict_move_kv4_kernel<128>, grid, m, stream);
+    return launch_move(src.b == 64 ? evict_move_kv4_kernel<64> : evict_move_kv4_kernel<128>, grid, kMove4Threads, m,
+                       stream);
 }
 
 }  // namespace sba
