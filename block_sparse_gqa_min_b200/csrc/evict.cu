@@ -16,7 +16,7 @@
 //  - gather kernels: one CTA per (destination block, KV head, sequence) moves the rows (whole rows,
 //    16 bytes a lane, all loads of a thread issued before its first store), the accumulators, and forms
 //    the block's Quest descriptor from the keys it holds in registers.  262144 bf16 rows: 48 us, 5.6 TB/s
-//    read and written; as many four-bit rows: 27 us (a kept row's 144 bytes lie in four pieces that cost 256
+//    read and written; as many four-bit rows: 26 us (a kept row's 144 bytes lie in four pieces that cost 256
 //    bytes of DRAM access).
 #include <math.h>
 
