@@ -74,7 +74,7 @@ __device__ __forceinline__ Share share_of(int units, int cta, int lane, Work wor
     r.unit = r.at = 0;
     if (r.left == 0) return r;
     int64_t at = r.start;
-    for (;; r.unit += 32) {
+    for (; r.unit < units; r.unit += 32) {
         const int mine = r.unit == 0 ? first : r.unit + lane < units ? work(r.unit + lane) : 0;
         int upto = mine;
 #pragma unroll
@@ -91,6 +91,8 @@ __device__ __forceinline__ Share share_of(int units, int cta, int lane, Work wor
         }
         at -= __shfl_sync(0xffffffffu, upto, 31);
     }
+    r.left = 0;  // (the lengths changed while they were being added up)
+    return r;
 }
 
 // 2^x; results below the normal range become 0.

@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
         return n < 0 ? 0 : min(n, a.n_max);
     };
     Share share{};
+    const int units = a.B * a.H_kv * a.row_groups;
     if constexpr (kShared) {
-        const int units = a.B * a.H_kv * a.row_groups;
         auto strips = [&](int u) {
             u /= a.row_groups;
             return max(1, blocks(u / a.H_kv, u % a.H_kv, a.sel_idx ? 0 : length(u / a.H_kv)) * spb);
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
 
     int64_t base = kShared ? share.start - share.at : 0;  // first strip of the unit, among all units'
     int left = kShared ? share.left : 1, at = kShared ? share.at : 0, unit = kShared ? share.unit : 0;
-    while (left > 0) {
+    while (left > 0 && unit < units) {
         int s, h, rg = 0;
         if constexpr (kShared) {
             s = unit / (a.H_kv * a.row_groups);

@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
         at = share.at;
         left = share.left;
     }
-    while (left > 0) {
+    while (left > 0 && unit < a.B * a.H_kv) {
         const int s = kShared ? unit / a.H_kv : (int)blockIdx.z, h = kShared ? unit % a.H_kv : (int)blockIdx.y;
         const int len = length(s), N = blocks_of(len, a.b), nb = blocks(unit, len), T = nb * tpb;
         const int32_t* sel = a.sel_idx ? a.sel_idx + (int64_t)unit * a.n_max : nullptr;
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     uint32_t phase = 0;
     bool alive = true;
 
-    for (; left > 0; ++unit, at = 0) {
+    for (; left > 0 && unit < units; ++unit, at = 0) {
         const int s = unit / a.H_kv, h = unit % a.H_kv;
         const int len = length(s), N = blocks_of(len, a.b), nb = blocks(unit);
         const int32_t* sel = a.sel_idx ? a.sel_idx + (int64_t)unit * a.n_max : nullptr;
