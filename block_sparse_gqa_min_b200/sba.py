@@ -452,12 +452,13 @@ class Cache4:
     def B(self) -> int:
         return int(self.seq_lens.shape[0])
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_struct", None)  # a replaced tensor has another address; in-place updates keep it
+
     def struct(self) -> sba_cache4:
-        # rebuilt only when a tensor of the cache is replaced (in-place updates keep the pointers)
-        key = (id(self.kv), id(self.block_table), id(self.seq_lens), id(self.desc), id(self.status), self.H_q,
-               self.max_blocks, self.max_len)
-        cached = self.__dict__.get("_struct")
-        if cached is None or cached[0] != key:
+        st = self.__dict__.get("_struct")
+        if st is None:
             if self.kv.dim() != 4 or self.kv.shape[3] != STRIP_BYTES:
                 raise ValueError(f"kv must be uint8 [num_pages][H_kv][b/32][{STRIP_BYTES}]")
             if not self.kv.is_cuda:
@@ -469,10 +470,8 @@ class Cache4:
                             self.d, self.b, self.max_blocks, self.num_pages, self.max_len,
                             _tensor(self.desc, torch.bfloat16, dev, self.num_pages * self.H_kv * 2 * self.d, "desc"),
                             _tensor(self.status, torch.int32, dev, 1, "status"))
-            # the tensors stay alive beside the key, so that an id is not met again on another one
-            cached = (key, st, (self.kv, self.block_table, self.seq_lens, self.desc, self.status))
-            self.__dict__["_struct"] = cached
-        return cached[1]
+            self.__dict__["_struct"] = st
+        return st
 
 
 def _tensor(t: Optional[torch.Tensor], dtype: torch.dtype, device: int, least: int, name: str):

@@ -217,6 +217,11 @@ def test_binding_takes_device_tensors_of_the_right_kind_only(monkeypatch):
         sba.sba_append_kv4(sba.Cache4(**good), rows, rows, lens)
     with pytest.raises(ValueError, match="kv must be"):
         sba.Cache4(**{**good, "kv": kv[..., :4600].contiguous()}).struct()
+    # a cache's struct follows its fields
+    c = sba.Cache4(**good)
+    c.__dict__["_struct"] = "old"
+    c.max_len = 128
+    assert "_struct" not in c.__dict__ and c.max_len == 128 and c.B == 1
     # what each argument has to be (device -1 is the CPU's)
     for t, why in ((torch.zeros(4), "int32"), (torch.zeros(3, dtype=torch.int32), "at least 4"),
                    (torch.zeros((4, 2), dtype=torch.int32).t(), "not contiguous")):
