@@ -337,11 +337,12 @@ int check_cache4(const sba_cache4* c) {
 }
 
 // Arguments of the calls that attend with M query tokens over a selection or (sel_idx NULL) all blocks.
-int check_attend(int H_q, int H_kv, const void* q, int32_t M, const int32_t* sel_idx, const int32_t* sel_cnt,
+int check_attend(int B, int H_q, int H_kv, const void* q, int32_t M, const int32_t* sel_idx, const int32_t* sel_cnt,
                  int32_t n_max, float softmax_scale) {
     if (!q || !aligned16(q) || M < 1 || M > kMaxQueryTokens || !good_scale(softmax_scale)) return SBA_ERR_INVALID_ARG;
     if (sel_idx ? (!sel_cnt || n_max < 1) : (sel_cnt != nullptr || n_max != 0)) return SBA_ERR_INVALID_ARG;
-    if ((int64_t)H_kv * (((int64_t)M * (H_q / H_kv) + 7) / 8) > 65535) return SBA_ERR_UNSUPPORTED;
+    const int64_t groups = (int64_t)H_kv * (((int64_t)M * (H_q / H_kv) + 7) / 8);
+    if (groups > 65535 || groups * B >= (int64_t)1 << 31) return SBA_ERR_UNSUPPORTED;
     return SBA_OK;
 }
 
@@ -412,7 +413,7 @@ int sba_decode_kv4(const sba_cache4* c, const void* q, int32_t M, const int32_t*
                    size_t ws_bytes, void* stream) {
     int rc = check_cache4(c);
     if (rc != SBA_OK) return rc;
-    rc = check_attend(c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
+    rc = check_attend(c->B, c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
     if (rc != SBA_OK) return rc;
     if (!out || !aligned16(out) || (out_dtype != SBA_OUT_F32 && out_dtype != SBA_OUT_BF16)) return SBA_ERR_INVALID_ARG;
     if (!ws || !aligned16(ws) || ws_bytes < decode_kv4_workspace_bytes(*c, M, n_max)) return SBA_ERR_WORKSPACE;
@@ -425,7 +426,7 @@ int sba_accumulate_weights(const sba_cache* c, const void* q, int32_t M, const i
                            const float* lse, const float* acc_in, float* acc_out, void* stream) {
     int rc = check_cache(c);
     if (rc != SBA_OK) return rc;
-    rc = check_attend(c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
+    rc = check_attend(c->B, c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
     if (rc != SBA_OK) return rc;
     if (gate_bias && (!sel_idx || M != 1)) return SBA_ERR_INVALID_ARG;
     rc = check_weights(lse, acc_in, acc_out);
@@ -440,7 +441,7 @@ int sba_accumulate_weights_kv4(const sba_cache4* c, const void* q, int32_t M, co
                                const float* acc_in, float* acc_out, void* stream) {
     int rc = check_cache4(c);
     if (rc != SBA_OK) return rc;
-    rc = check_attend(c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
+    rc = check_attend(c->B, c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
     if (rc != SBA_OK) return rc;
     rc = check_weights(lse, acc_in, acc_out);
     if (rc != SBA_OK) return rc;

@@ -21,7 +21,7 @@
 //    conversion delivers the token pairs that the A operand wants.
 //  - Q enters as f16 after each row is scaled by a power of two to a maximum in [1, 2), P as f16 (2^8
 //    at the running maximum) plus, for fp32 outputs, the f16 of what that rounding left: bf16 outputs
-//    round at 2^-9, the f16 of P at 2^-12.
+//    round by up to 2^-8, the f16 of P by up to 2^-11.
 // Every warp works alone: it walks strips of 32 tokens (4608 bytes, one bulk copy each) through a
 // ring of its own, so no warp waits for another until the merge.
 //
@@ -45,7 +45,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kFlush = 8;  // strips after which fp32 outputs move their sums out of the MMA accumulators
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kMostParts = 128;           // CTAs for each unit, at most: merging more takes longer than they save
+constexpr int kMostParts = 128;           // CTAs a unit on average, at most: merging more takes longer than they save
 constexpr int kRowStride = kHeadDim + 4;  // floats between rows of the merge buffer
 constexpr float kPShift = 8.f;            // P is exp2((s - max) * scale + 8): small weights stay normal f16 numbers
 constexpr float kSlack = 7.f;             // the running maximum moves only when exceeded by 2^7 (P <= 2^15)
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
     pdl_trigger();
 
     // ---- this CTA's share of all units' strips (a unit without any counts one, so that its rows get
-    // written); no fewer than a strip a warp, and no unit in more than kMostParts parts ----
+    // written); no fewer than a strip a warp, and no more than kMostParts CTAs a unit on average ----
     auto length = [&](int s) { return max(0, min(__ldca(a.seq_lens + s), a.max_blocks * a.b)); };
     auto blocks = [&](int s, int h, int len) {
         if (!a.sel_idx) return blocks_of(len, a.b);

@@ -471,7 +471,9 @@ int sba_score_select_kv4(const sba_cache4 *c, const void *q, int32_t M, const sb
  * ws        device workspace of at least sba_decode_kv4_workspace_size() bytes, 16-byte aligned,
  *           ZERO-FILLED before its first use; every completed call leaves its counters at zero again, so
  *           calls of any shapes may use it one after another.  Calls that share a workspace must not run
- *           concurrently (a graph that holds calls and eager calls beside it: a workspace each). */
+ *           concurrently (a graph that holds calls and eager calls beside it: a workspace each).
+ * SBA_ERR_UNSUPPORTED where H_kv * ceil(M*G/8) passes 65535, or B times that 2^31 - 1 (as for the
+ * accumulated weights below). */
 size_t sba_decode_kv4_workspace_size(const sba_cache4 *c, int32_t M, int32_t n_max);
 int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t *sel_idx, const int32_t *sel_cnt,
                    int32_t n_max, float softmax_scale, void *out, int32_t out_dtype, float *lse_out, void *ws,

@@ -161,6 +161,8 @@ def test_bad_decode():
     assert need > 0 and call(ws=None) == WS and call(size=need - 1) == WS and call(ws=0x8008) == WS
     assert lib.sba_decode_kv4_workspace_size(c4(), 0, 0) == 0 and lib.sba_decode_kv4_workspace_size(c4(), 1, -1) == 0
     assert lib.sba_decode_kv4_workspace_size(c4(), 4, 0) > need                         # 16 rows instead of 8
+    wide = dict(B=40000, H_q=508, H_kv=508, max_blocks=1, num_pages=60000, max_len=64, block_table=0x9000)
+    assert lib.sba_decode_kv4(c4(**wide, b=64), 0x5000, 1024, None, None, 0, 0.1, 0x6000, 0, None, 0x8000, 1 << 40, None) == UNS
     gate = ctypes.byref(sba.select_params(16, 2, scorer=sba.SBA_SCORER_GATE))
     assert lib.sba_score_select_kv4(c4(), 0x5000, 1, gate, 0x6000, 0x7000, 16, 0x8000, 1 << 20, None) == UNS
     p = ctypes.byref(sba.select_params(16, 2))
