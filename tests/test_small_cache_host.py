@@ -247,3 +247,20 @@ def test_binding_takes_device_tensors_of_the_right_kind_only(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         sba._current(0, None)
+
+
+def test_a_replaced_tensor_is_seen_even_where_its_identity_comes_again(monkeypatch):
+    # an object's identity may be a dead one's: the struct must not be looked up by it
+    monkeypatch.setattr(sba, "_ptr", lambda t: None if t is None else ctypes.c_void_p(t.data_ptr()))
+    k = torch.zeros((4, 2, 64, 128), dtype=torch.bfloat16)
+    c = sba.Cache(k=k, v=torch.zeros_like(k), seq_lens=torch.zeros(1, dtype=torch.int32), H_q=4, max_blocks=4,
+                  max_len=256)
+    desc = torch.zeros(64, dtype=torch.bfloat16)
+    c.desc = desc
+    assert c.struct().desc == desc.data_ptr() and c.struct() is c.struct()
+    monkeypatch.setattr(sba, "id", lambda t: 0, raising=False)
+    c.struct()
+    c.desc = torch.ones(64, dtype=torch.bfloat16)
+    assert c.struct().desc == c.desc.data_ptr() != desc.data_ptr()
+    c.desc = None
+    assert c.struct().desc is None
