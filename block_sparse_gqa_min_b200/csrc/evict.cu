@@ -59,7 +59,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     extern __shared__ __align__(16) uint32_t dyn[];
     uint32_t* keys = dyn + kSelFixed / 4;
     __shared__ uint32_t scan[kSelWarps];
-    __shared__ uint32_t found[2];  // digit of the threshold, tokens still to take at it
+    __shared__ uint32_t found[3];  // digit of the threshold, tokens still to take at it, tokens that share it
+    __shared__ uint32_t listed;    // tokens of this CTA in the list of the last two digits
     __shared__ uint2 warp_n[kSelWarps];
     __shared__ uint2 total;  // tokens of this CTA above and at the threshold
 
@@ -67,6 +68,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     const int h = blockIdx.y, s = blockIdx.z;
     const uint32_t rank = cluster_rank(), C = cluster_size();
     for (int i = tid; i < kSelFixed / 4; i += kSelThreads) dyn[i] = 0;
+    if (tid == 0) listed = 0;
     pdl_wait();
     const int n = clamped_len(a.seq_lens, s, a.max_blocks, a.b);
     const int keep = a.p.n_keep;
@@ -153,11 +155,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         dyn[tid] = c;
     }
     uint32_t prefix = 0, left = (uint32_t)k;  // left: tokens to take among those whose key starts with prefix
+    bool few = false;                         // every thread of every CTA holds at most one of them: low_key
+    uint32_t low_key = ~0u;
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
         uint32_t* hist = pass == 0 ? dyn : dyn + kCopies * kCopyStride + (pass - 1) * kBins;
-        if (pass > 0) {
-            const int shift = 24 - 8 * pass;
+        const int shift = 24 - 8 * pass;
+        if (few) {
+            if (low_key >> (shift + 8) == (prefix & (0xffffu >> (shift + 8)))) atomicAdd(&hist[(low_key >> shift) & 255u], 1u);
+        } else if (pass > 0) {
 #pragma unroll 4
             for (int i = tid; i < nq; i += kSelThreads) {
                 const uint4 r = quad(i);
@@ -167,15 +173,22 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
                 if (r.w >> (shift + 8) == prefix && r.w) atomicAdd(&hist[(r.w >> shift) & 255u], 1u);
             }
         }
-        cluster_sync();
+        if (few)
+            __syncthreads();
+        else
+            cluster_sync();
         // digits from the top: thread d of the first eight warps takes bin 255 - d
         uint32_t mine = 0, sum = 0;
         if (tid < kBins) {
-            uint32_t c[kMaxCluster];  // all loads before the first sum
+            if (few) {
+                mine = hist[kBins - 1 - tid];
+            } else {
+                uint32_t c[kMaxCluster];  // all loads before the first sum
 #pragma unroll
-            for (uint32_t r = 0; r < kMaxCluster; ++r) c[r] = r < C ? ld_peer_u32(peer_addr(&hist[kBins - 1 - tid], r)) : 0u;
+                for (uint32_t r = 0; r < kMaxCluster; ++r) c[r] = r < C ? ld_peer_u32(peer_addr(&hist[kBins - 1 - tid], r)) : 0u;
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) mine += c[r];
+                for (int r = 0; r < kMaxCluster; ++r) mine += c[r];
+            }
             sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -193,11 +206,46 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
             if (before < left && before + mine >= left) {
                 found[0] = kBins - 1 - tid;
                 found[1] = left - before;
+                found[2] = mine;
             }
         }
         __syncthreads();
         prefix = (prefix << 8) | found[0];
         left = found[1];
+        if (pass == 1 && found[2] <= kSelThreads) {
+            // The tokens that share the threshold's upper 16 bits have a thread each: every CTA lists its own
+            // (where the first histogram was: the peers have read it), then takes one of all of them, and the
+            // last two digits need no other CTA.
+            few = true;
+#pragma unroll 4
+            for (int i = tid; i < nq; i += kSelThreads) {
+                const uint4 r = quad(i);
+                const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (v[x] >> 16 != prefix || !v[x]) continue;
+                    const uint32_t to = atomicAdd(&listed, 1u);
+                    if (to < kSelThreads) dyn[to] = v[x] & 0xffffu;
+                }
+            }
+            cluster_sync();
+            const uint32_t theirs = lane < C ? ld_peer_u32(peer_addr(&listed, lane)) : 0u;
+            uint32_t upto = theirs;
+#pragma unroll
+            for (int o = 1; o < kMaxCluster; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            uint32_t owner = 0, from = 0;  // the last CTA whose list starts at or before this thread
+            for (uint32_t r = 1; r < C; ++r) {
+                const uint32_t at = __shfl_sync(0xffffffffu, upto, r - 1);
+                if ((uint32_t)tid >= at) {
+                    owner = r;
+                    from = at;
+                }
+            }
+            if ((uint32_t)tid < __shfl_sync(0xffffffffu, upto, C - 1)) low_key = ld_peer_u32(peer_addr(&dyn[tid - from], owner));
+        }
         __syncthreads();
     }
     const uint32_t T = prefix;
