@@ -38,6 +38,7 @@ constexpr int kCopies = 8;                  // of the first histogram, by lane: 
 constexpr int kCopyStride = kBins + 4;      // words: the copies of a bin in different banks
 constexpr int kSelFixed = (kCopies * kCopyStride + 3 * kBins) * 4;
 constexpr int kSelMaxKeys = (226 * 1024 - kSelFixed) / 16 * 4;  // keys of a slice kept in shared memory
+static_assert(kSelMaxKeys <= 15 * 4 * kSelThreads, "a thread's run of held keys has a bit each");
 constexpr int kMoveThreads = 256;
 
 struct SelectArgs {
@@ -155,6 +156,25 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         dyn[tid] = c;
     }
     uint32_t prefix = 0, left = (uint32_t)k;  // left: tokens to take among those whose key starts with prefix
+    // Runs: where all keys are held, a thread keeps in two masks which tokens of its own run of quads (an odd
+    // number of them: its 16-byte reads then fall in different banks) are above the prefix and which are at it,
+    // so that after the second pass only those at it are looked at again.
+    const bool runs = 4 * nq <= cap;
+    const int per = ((nq + kSelThreads - 1) / kSelThreads) | 1;
+    const int i0 = min(nq, tid * per), i1 = min(nq, i0 + per);
+    uint64_t above = 0, at = 0;
+    auto sift = [&](uint32_t top, int shift, auto same) {
+        for (uint64_t rest = at; rest; rest &= rest - 1) {
+            const int bit = __ffsll((long long)rest) - 1;
+            const uint32_t v = keys[4 * i0 + bit], u = v >> shift;
+            if (u == top) {
+                same(v);
+            } else {
+                at ^= (uint64_t)1 << bit;
+                above |= (uint64_t)(u > top) << bit;
+            }
+        }
+    };
     bool few = false;                         // every thread of every CTA holds at most one of them: low_key
     uint32_t low_key = ~0u;
 #pragma unroll 1
@@ -163,6 +183,26 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         const int shift = 24 - 8 * pass;
         if (few) {
             if (low_key >> (shift + 8) == (prefix & (0xffffu >> (shift + 8)))) atomicAdd(&hist[(low_key >> shift) & 255u], 1u);
+        } else if (pass == 1 && runs) {
+            const uint32_t lo = max(1u, prefix << 24), hi = prefix << 24 | 0xffffffu;
+#pragma unroll 2
+            for (int i = i0; i < i1; ++i) {
+                const uint4 r = *reinterpret_cast<const uint4*>(keys + 4 * i);
+                const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+                uint32_t bg = 0, be = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (v[x] > hi) bg |= 1u << x;
+                    if (v[x] - lo <= hi - lo) {
+                        be |= 1u << x;
+                        atomicAdd(&hist[(v[x] >> 16) & 255u], 1u);
+                    }
+                }
+                above |= (uint64_t)bg << 4 * (i - i0);
+                at |= (uint64_t)be << 4 * (i - i0);
+            }
+        } else if (pass > 1 && runs) {
+            sift(prefix, shift + 8, [&](uint32_t v) { atomicAdd(&hist[(v >> shift) & 255u], 1u); });
         } else if (pass > 0) {
 #pragma unroll 4
             for (int i = tid; i < nq; i += kSelThreads) {
@@ -217,15 +257,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
             // (where the first histogram was: the peers have read it), then takes one of all of them, and the
             // last two digits need no other CTA.
             few = true;
+            auto list = [&](uint32_t v) {
+                const uint32_t to = atomicAdd(&listed, 1u);
+                if (to < kSelThreads) dyn[to] = v & 0xffffu;
+            };
+            if (runs) {
+                sift(prefix, 16, list);
+            } else {
 #pragma unroll 4
-            for (int i = tid; i < nq; i += kSelThreads) {
-                const uint4 r = quad(i);
-                const uint32_t v[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (v[x] >> 16 != prefix || !v[x]) continue;
-                    const uint32_t to = atomicAdd(&listed, 1u);
-                    if (to < kSelThreads) dyn[to] = v[x] & 0xffffu;
+                for (int i = tid; i < nq; i += kSelThreads) {
+                    const uint4 r = quad(i);
+                    if (r.x >> 16 == prefix && r.x) list(r.x);
+                    if (r.y >> 16 == prefix && r.y) list(r.y);
+                    if (r.z >> 16 == prefix && r.z) list(r.z);
+                    if (r.w >> 16 == prefix && r.w) list(r.w);
                 }
             }
             cluster_sync();
@@ -250,22 +295,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     }
     const uint32_t T = prefix;
 
-    // ---- tokens above and at the threshold, in order: every thread takes a run of quads (an odd number of
-    // them: its 16-byte reads then fall in different banks), so that nothing has to be counted across lanes
-    // but the threads' totals ----
-    const int per = ((nq + kSelThreads - 1) / kSelThreads) | 1;
-    const int i0 = min(nq, tid * per), i1 = min(nq, i0 + per);
-    uint64_t above = 0, at = 0;  // its tokens above and at the threshold, a bit each, where they fit
+    // ---- tokens above and at the threshold, in order: every thread has a run of quads, so that nothing has to
+    // be counted across lanes but the threads' totals ----
     uint32_t gt = 0, eq = 0;
+    if (runs) {
+        sift(T, 0, [](uint32_t) {});
+        gt = __popcll(above);
+        eq = __popcll(at);
+    } else {
 #pragma unroll 4
-    for (int i = i0; i < i1; ++i) {
-        const uint4 r = quad(i);
-        const uint32_t bg = (r.x > T) | (r.y > T) << 1 | (r.z > T) << 2 | (r.w > T) << 3;
-        const uint32_t be = (r.x == T) | (r.y == T) << 1 | (r.z == T) << 2 | (r.w == T) << 3;
-        above |= (uint64_t)bg << (4 * (i - i0) & 63);
-        at |= (uint64_t)be << (4 * (i - i0) & 63);
-        gt += __popc(bg);
-        eq += __popc(be);
+        for (int i = i0; i < i1; ++i) {
+            const uint4 r = quad(i);
+            gt += (r.x > T) + (r.y > T) + (r.z > T) + (r.w > T);
+            eq += (r.x == T) + (r.y == T) + (r.z == T) + (r.w == T);
+        }
     }
     uint32_t g = gt, e = eq;  // the tokens of this thread and those before it: warp, CTA, cluster
 #pragma unroll
@@ -291,7 +334,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     g += __reduce_add_sync(0xffffffffu, n_c.x);
     e += __reduce_add_sync(0xffffffffu, n_c.y);
     pdl_trigger();
-    if (per <= 16) {
+    if (runs) {
         for (uint64_t rest = above | at; rest; rest &= rest - 1) {
             const int bit = __ffsll((long long)rest) - 1;
             const bool is_at = at >> bit & 1;
