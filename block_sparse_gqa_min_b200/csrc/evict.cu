@@ -101,10 +101,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     auto keys_of = [&](int i, float4 w) {
         const int t = 4 * (q0 + i);
         uint4 r;
-        r.x = t < sink || t >= last ? 0u : w.x != w.x ? 1u : orderable_key(w.x);
-        r.y = t + 1 < sink || t + 1 >= last ? 0u : w.y != w.y ? 1u : orderable_key(w.y);
-        r.z = t + 2 < sink || t + 2 >= last ? 0u : w.z != w.z ? 1u : orderable_key(w.z);
-        r.w = t + 3 < sink || t + 3 >= last ? 0u : w.w != w.w ? 1u : orderable_key(w.w);
+        r.x = w.x != w.x ? 1u : orderable_key(w.x);
+        r.y = w.y != w.y ? 1u : orderable_key(w.y);
+        r.z = w.z != w.z ? 1u : orderable_key(w.z);
+        r.w = w.w != w.w ? 1u : orderable_key(w.w);
+        if (t < sink || t + 3 >= last) {
+            if (t < sink || t >= last) r.x = 0;
+            if (t + 1 < sink || t + 1 >= last) r.y = 0;
+            if (t + 2 < sink || t + 2 >= last) r.z = 0;
+            if (t + 3 < sink || t + 3 >= last) r.w = 0;
+        }
         return r;
     };
     auto quad = [&](int i) -> uint4 {
@@ -112,42 +118,55 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     };
 
     __syncthreads();
-    // ---- read the slice; histogram of the top 8 bits ----
+    // ---- read the slice; histogram of the top 8 bits.  Asynchronous copies (what little L1 the keys leave could
+    // not hold this many loads in flight), kLoads quads a thread at a time: one batch is counted while the next
+    // is copied and the pages of the one after are looked up ----
     uint32_t* own = dyn + (lane & (kCopies - 1)) * kCopyStride;
-    // (asynchronous copies: what little L1 the keys leave could not hold this many loads in flight)
-    const int held = min(nq, cap / 4);
-    constexpr int kLoads = 8;  // page lookups in flight
-    for (int i0 = tid; i0 < held; i0 += kLoads * kSelThreads) {
-        int cell[kLoads];
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x) cell[x] = i0 + x * kSelThreads < held ? cell_of(i0 + x * kSelThreads) : 0;
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x) {
-            const int i = i0 + x * kSelThreads;
-            if (i >= held) break;
-            if (cell[x] >= 0) {
-                cp_async_16(keys + 4 * i, a.acc + cell[x]);
-            } else {
-                report(a.status, SBA_DEV_BAD_PAGE);
-                *reinterpret_cast<float4*>(keys + 4 * i) = weights_of(-1);
-            }
-        }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // this thread's own, and it reads no other's
-#pragma unroll 4
-    for (int i = tid; i < nq; i += kSelThreads) {
-        uint4 r;
-        if (i < held) {
-            r = keys_of(i, *reinterpret_cast<const float4*>(keys + 4 * i));
-            *reinterpret_cast<uint4*>(keys + 4 * i) = r;
-        } else {
-            r = quad(i);
-        }
+    auto count = [&](uint4 r) {
         if (r.x) atomicAdd(&own[r.x >> 24], 1u);
         if (r.y) atomicAdd(&own[r.y >> 24], 1u);
         if (r.z) atomicAdd(&own[r.z >> 24], 1u);
         if (r.w) atomicAdd(&own[r.w >> 24], 1u);
+    };
+    const int held = min(nq, cap / 4);
+    constexpr int kLoads = 4, kStep = kLoads * kSelThreads;
+    int cell[kLoads];
+    auto look_up = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) cell[x] = i + x * kSelThreads < held ? cell_of(i + x * kSelThreads) : 0;
+    };
+    auto copy = [&](int i) {
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            uint32_t* to = keys + 4 * (i + x * kSelThreads);
+            if (i + x * kSelThreads >= held) break;
+            if (cell[x] >= 0) {
+                cp_async_16(to, a.acc + cell[x]);
+            } else {
+                report(a.status, SBA_DEV_BAD_PAGE);
+                *reinterpret_cast<float4*>(to) = weights_of(-1);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    look_up(tid);
+    copy(tid);
+    look_up(tid + kStep);
+    for (int b0 = tid; b0 < held; b0 += kStep) {
+        copy(b0 + kStep);
+        look_up(b0 + 2 * kStep);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");  // this thread's own, and it reads no other's
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            const int i = b0 + x * kSelThreads;
+            if (i >= held) break;
+            const uint4 r = keys_of(i, *reinterpret_cast<const float4*>(keys + 4 * i));
+            *reinterpret_cast<uint4*>(keys + 4 * i) = r;
+            count(r);
+        }
     }
+#pragma unroll 2
+    for (int i = tid + (held - tid + kSelThreads - 1) / kSelThreads * kSelThreads; i < nq; i += kSelThreads) count(quad(i));
     __syncthreads();
     if (tid < kBins) {
         uint32_t c = 0;
