@@ -181,18 +181,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     const bool runs = 4 * nq <= cap;
     const int per = ((nq + kSelThreads - 1) / kSelThreads) | 1;
     const int i0 = min(nq, tid * per), i1 = min(nq, i0 + per);
-    uint64_t above = 0, at = 0;
+    uint32_t above[2] = {0, 0}, at[2] = {0, 0};
     auto sift = [&](uint32_t top, int shift, auto same) {
-        for (uint64_t rest = at; rest; rest &= rest - 1) {
-            const int bit = __ffsll((long long)rest) - 1;
-            const uint32_t v = keys[4 * i0 + bit], u = v >> shift;
-            if (u == top) {
-                same(v);
-            } else {
-                at ^= (uint64_t)1 << bit;
-                above |= (uint64_t)(u > top) << bit;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            for (uint32_t rest = at[y]; rest; rest &= rest - 1) {
+                const int bit = __ffs(rest) - 1;
+                const uint32_t v = keys[4 * i0 + 32 * y + bit], u = v >> shift;
+                if (u == top) {
+                    same(v);
+                } else {
+                    at[y] ^= 1u << bit;
+                    if (u > top) above[y] |= 1u << bit;
+                }
             }
-        }
     };
     bool few = false;                         // every thread of every CTA holds at most one of them: low_key
     uint32_t low_key = ~0u;
@@ -204,22 +206,23 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
             if (low_key >> (shift + 8) == (prefix & (0xffffu >> (shift + 8)))) atomicAdd(&hist[(low_key >> shift) & 255u], 1u);
         } else if (pass == 1 && runs) {
             const uint32_t lo = max(1u, prefix << 24), hi = prefix << 24 | 0xffffffu;
-#pragma unroll 2
-            for (int i = i0; i < i1; ++i) {
-                const uint4 r = *reinterpret_cast<const uint4*>(keys + 4 * i);
-                const uint32_t v[4] = {r.x, r.y, r.z, r.w};
-                uint32_t bg = 0, be = 0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (v[x] > hi) bg |= 1u << x;
-                    if (v[x] - lo <= hi - lo) {
-                        be |= 1u << x;
-                        atomicAdd(&hist[(v[x] >> 16) & 255u], 1u);
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    const int i = i0 + 8 * y + z;
+                    if (i >= i1) break;
+                    const uint4 r = *reinterpret_cast<const uint4*>(keys + 4 * i);
+                    const uint32_t v[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        if (v[x] > hi) above[y] |= 1u << (4 * z + x);
+                        if (v[x] - lo <= hi - lo) {
+                            at[y] |= 1u << (4 * z + x);
+                            atomicAdd(&hist[(v[x] >> 16) & 255u], 1u);
+                        }
                     }
                 }
-                above |= (uint64_t)bg << 4 * (i - i0);
-                at |= (uint64_t)be << 4 * (i - i0);
-            }
         } else if (pass > 1 && runs) {
             sift(prefix, shift + 8, [&](uint32_t v) { atomicAdd(&hist[(v >> shift) & 255u], 1u); });
         } else if (pass > 0) {
@@ -319,8 +322,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     uint32_t gt = 0, eq = 0;
     if (runs) {
         sift(T, 0, [](uint32_t) {});
-        gt = __popcll(above);
-        eq = __popcll(at);
+        gt = __popc(above[0]) + __popc(above[1]);
+        eq = __popc(at[0]) + __popc(at[1]);
     } else {
 #pragma unroll 4
         for (int i = i0; i < i1; ++i) {
@@ -354,13 +357,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     e += __reduce_add_sync(0xffffffffu, n_c.y);
     pdl_trigger();
     if (runs) {
-        for (uint64_t rest = above | at; rest; rest &= rest - 1) {
-            const int bit = __ffsll((long long)rest) - 1;
-            const bool is_at = at >> bit & 1;
-            if (!is_at || e < left) kept[sink + g + min(e, left)] = 4 * (q0 + i0) + bit;
-            g += !is_at;
-            e += is_at;
-        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            for (uint32_t rest = above[y] | at[y]; rest; rest &= rest - 1) {
+                const int bit = __ffs(rest) - 1;
+                const bool is_at = at[y] >> bit & 1;
+                if (!is_at || e < left) kept[sink + g + min(e, left)] = 4 * (q0 + i0) + 32 * y + bit;
+                g += !is_at;
+                e += is_at;
+            }
     } else if (gt + eq > 0) {
         for (int i = i0; i < i1; ++i) {
             const uint4 r = quad(i);
