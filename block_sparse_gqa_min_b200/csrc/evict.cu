@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         if (r.w) atomicAdd(&own[r.w >> 24], 1u);
     };
     const int held = min(nq, cap / 4);
-    constexpr int kLoads = 4, kStep = kLoads * kSelThreads;
+    constexpr int kLoads = 2, kStep = kLoads * kSelThreads;
     int cell[kLoads];
     auto look_up = [&](int i) {
 #pragma unroll
