@@ -56,6 +56,12 @@ __device__ __forceinline__ int clamped_len(const int32_t* seq_lens, int s, int m
     return max(0, min(__ldca(seq_lens + s), max_blocks * b));
 }
 
+// Larger for a larger weight, the same for both zeros; 1 for a NaN.
+__device__ __forceinline__ uint32_t key_of(float w) {
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return w != w ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a, int cap) {
     extern __shared__ __align__(16) uint32_t dyn[];
     uint32_t* keys = dyn + kSelFixed / 4;
@@ -101,10 +107,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     auto keys_of = [&](int i, float4 w) {
         const int t = 4 * (q0 + i);
         uint4 r;
-        r.x = w.x != w.x ? 1u : orderable_key(w.x);
-        r.y = w.y != w.y ? 1u : orderable_key(w.y);
-        r.z = w.z != w.z ? 1u : orderable_key(w.z);
-        r.w = w.w != w.w ? 1u : orderable_key(w.w);
+        r.x = key_of(w.x);
+        r.y = key_of(w.y);
+        r.z = key_of(w.z);
+        r.w = key_of(w.w);
         if (t < sink || t + 3 >= last) {
             if (t < sink || t >= last) r.x = 0;
             if (t + 1 < sink || t + 1 >= last) r.y = 0;
@@ -122,11 +128,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
     // not hold this many loads in flight), kLoads quads a thread at a time: one batch is counted while the next
     // is copied and the pages of the one after are looked up ----
     uint32_t* own = dyn + (lane & (kCopies - 1)) * kCopyStride;
-    auto count = [&](uint4 r) {
-        if (r.x) atomicAdd(&own[r.x >> 24], 1u);
-        if (r.y) atomicAdd(&own[r.y >> 24], 1u);
-        if (r.z) atomicAdd(&own[r.z >> 24], 1u);
-        if (r.w) atomicAdd(&own[r.w >> 24], 1u);
+    auto count = [&](uint4 r) {  // tokens that are not ranked too: in the last bin, whose number decides nothing
+        atomicAdd(&own[r.x >> 24], 1u);
+        atomicAdd(&own[r.y >> 24], 1u);
+        atomicAdd(&own[r.z >> 24], 1u);
+        atomicAdd(&own[r.w >> 24], 1u);
     };
     const int held = min(nq, cap / 4);
     constexpr int kLoads = 2, kStep = kLoads * kSelThreads;
