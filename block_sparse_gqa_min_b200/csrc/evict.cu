@@ -9,10 +9,13 @@
 //    shared memory (as far as they fit; the rest is read again from L2).  The threshold is found by a
 //    radix select, 8 bits a pass: a shared-memory histogram of the slice, then one cluster barrier,
 //    after which every CTA adds the cluster's histograms through distributed shared memory and finds
-//    the same digit (256 bins: with 2048 and a pass less, reading ten peers' bins took 6 us a pass).  A
-//    count and an ordered write follow; no position depends on an atomic.  64 units of 32-64K tokens: 29 us,
-//    8 units of 512K: 37 us (reading 6, each pass 4, the count 5, the write 1.5): it is bound by the latency
-//    of these dependent passes, four bytes a token being read in 1-3 us.
+//    the same digit (256 bins: with 2048 and a pass less, reading ten peers' bins took 6 us a pass).  From the
+//    second pass on a thread knows its tokens above the prefix and at it as bits and looks at the latter only;
+//    once 1024 or fewer are left in the cluster, every CTA finds the last 16 bits alone.  An ordered write
+//    follows; no position depends on an atomic.  64 units of 32-64K tokens: 20 us, 8 units of 512K: 25 us
+//    (reading and counting 9, the second pass 5, the last digits 5, the write 3.5, barriers and digits the
+//    rest): it is bound by the instructions of the first two passes (10 CTAs a unit: 13 quads a thread) and the
+//    latency of what follows.
 //  - gather kernels: one CTA per (destination block, KV head, sequence) moves the rows (whole rows,
 //    16 bytes a lane, all loads of a thread issued before its first store), the accumulators, and forms
 //    the block's Quest descriptor from the keys it holds in registers.  262144 bf16 rows: 48 us, 5.6 TB/s

@@ -267,6 +267,33 @@ def test_evict_slices_longer_than_shared_memory():
         assert torch.equal(rows, moved)
 
 
+@pytest.mark.parametrize("H,n", [(1, 70000), (2, 9000), (80, 70000)])
+@pytest.mark.parametrize("near", [1, 1023, 1024, 1025, 6000])
+def test_evict_tokens_that_share_the_thresholds_upper_bits(H, n, near):
+    """Around 1024 weights whose upper 16 bits are the threshold's; slices held in shared memory and longer ones."""
+    b, sink, recent, more = 64, 3, 7, 50
+    keep = sink + recent + more + (near + 1) // 2
+    lay, dlay = layout([n], b, False, 1, slack=0), layout([keep], b, False, 2, slack=0)
+    g = torch.Generator(device="cuda").manual_seed(near)
+    acc = 0.5 * torch.rand((H, n), generator=g, device=DEV)
+    for h in range(H):
+        at = sink + torch.randperm(n - sink - recent, generator=g, device=DEV)[:near + more]
+        low = torch.randint(0, 1 << (16 if h % 2 == 0 else 3), (near,), generator=g, device=DEV)  # distinct, or ties
+        acc[h, at[:near]] = (0x3f800000 + low).to(torch.int32).view(torch.float32)
+        acc[h, at[near:]] = 2 + torch.rand(more, generator=g, device=DEV)
+    padded = torch.zeros((H, lay.pages * b), device=DEV)
+    padded[:, :n] = acc
+    pool = padded.reshape(H, lay.pages, b).transpose(0, 1).contiguous()
+    kv = torch.zeros((lay.pages, H, b // 32, 4608), dtype=torch.uint8, device=DEV)
+    src, dst = cache4(lay, kv, H_q=H, desc=False), cache4(dlay, torch.zeros((dlay.pages, H, b // 32, 4608), dtype=torch.uint8), H)
+    new_lens, kept = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros((1, H, keep), dtype=torch.int32, device=DEV)
+    sba.sba_evict_kv4(src, pool, sba.evict_params(keep, sink, recent), dst, new_lens, kept)
+    assert new_lens.tolist() == [keep] and int(src.status.item()) == 0
+    w, got = acc.cpu().numpy(), kept.cpu().numpy()
+    for h in {0, 1, H - 1} & set(range(H)):
+        assert np.array_equal(got[0, h], SC.keep(w[h], keep, sink, recent))
+
+
 def test_weights_past_four_gigabytes_and_understated_selection():
     """Key pages whose byte offsets do not fit 32 bits (bf16 and four bits, few rows and many), and selections
     shorter than their row."""
