@@ -361,7 +361,9 @@ int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* 
     if (dst.B != src.B || dst.H_kv != src.H_kv || dst.b != src.b) return SBA_ERR_INVALID_ARG;
     if ((int64_t)p->n_keep > (int64_t)dst.max_blocks * dst.b) return SBA_ERR_INVALID_ARG;
     // the lengths are read while the new ones are written, the rows while others are
-    if (new_lens == src.seq_lens || acc_dst == acc || (dst.desc && dst.desc == src.desc && !dst.block_table))
+    const intptr_t apart = reinterpret_cast<intptr_t>(new_lens) - reinterpret_cast<intptr_t>(src.seq_lens);
+    const intptr_t size = (intptr_t)src.B * 4;
+    if ((apart > -size && apart < size) || acc_dst == acc || (dst.desc && dst.desc == src.desc && !dst.block_table))
         return SBA_ERR_INVALID_ARG;
     if ((dst.k == src.k || dst.v == src.v) && !dst.block_table && !src.block_table) return SBA_ERR_INVALID_ARG;
     if (src.B > 65535 || src.H_kv > 65535) return SBA_ERR_UNSUPPORTED;

@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 if (v[x] < T) continue;
-                if (v[x] > T || e < left) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
+                // (keys that are read again could have changed: nothing is written past the row)
+                if ((v[x] > T || e < left) && sink + g + min(e, left) < keep) kept[sink + g + min(e, left)] = 4 * (q0 + i) + x;
                 g += v[x] > T;
                 e += v[x] == T;
             }

@@ -509,7 +509,7 @@ int sba_accumulate_weights_kv4(const sba_cache4 *c, const void *q, int32_t M, co
  *            descriptors of the blocks written; gate keys are not refreshed (call
  *            sba_update_descriptors for them).  Rows of dst past the kept ones are left as they were.
  * acc_dst    device fp32 [dst->num_pages][H_kv][b] or NULL: the kept tokens' weights; not acc itself.
- * new_lens   device int32 [B]: min(len_s, n_keep); not src->seq_lens itself.
+ * new_lens   device int32 [B]: min(len_s, n_keep); does not overlap src->seq_lens.
  * kept       device int32 [B][H_kv][n_keep]: the kept positions in src, ascending; entries past the
  *            new length are left as they were. */
 int sba_evict(const sba_cache *src, const float *acc, const sba_evict_params *p, const sba_cache *dst,

@@ -264,3 +264,11 @@ def test_a_replaced_tensor_is_seen_even_where_its_identity_comes_again(monkeypat
     assert c.struct().desc == c.desc.data_ptr() != desc.data_ptr()
     c.desc = None
     assert c.struct().desc is None
+
+
+def test_evict_refuses_new_lengths_that_overlap_the_old_ones():
+    lib = sba.load()
+    e = ctypes.byref(sba.evict_params(64))
+    big = dict(B=4, num_pages=256, H_kv=2)
+    for new in (0x3000, 0x3004, 0x300c, 0x2ffc, 0x2ff4):
+        assert lib.sba_evict(c16(**big), 0x5000, e, c16(k=0x100000, v=0x200000, desc=None, **big), None, new, 0x7000, None) == ARG
