@@ -20,16 +20,16 @@
 //    tokens' codes are interleaved as nibbles (four logic operations for eight results) so that the
 //    conversion delivers the token pairs that the A operand wants.
 //  - Q enters as f16 after each row is scaled by a power of two to a maximum in [1, 2), P as f16 (2^8
-//    at the running maximum) plus, for fp32 outputs, the f16 of what that rounding left: bf16 outputs
-//    round by up to 2^-8, the f16 of P by up to 2^-11.
+//    at the running maximum) plus the f16 of what that rounding left, whatever the output type: with one
+//    f16 alone 6-10% of bf16 outputs came out a step beside the rounding of the exact result.
 // Every warp works alone: it walks strips of 32 tokens (4608 bytes, one bulk copy each) through a
 // ring of its own, so no warp waits for another until the merge.
 //
-// Measured on B200: all tokens of 8 sequences of 32-64K, 32/8 heads, bf16 out: 103 us, 4.4 TB/s of the
-// cache, 67% of the copy bandwidth; it is bound by the instructions that turn codes into operands (610 a
-// strip and warp, the ALU pipe 52% busy, 2.4 instructions a cycle), not by memory (50%) or the MMAs
-// (24%).  Short launches are bound by their dependent steps: 64 blocks of 64 tokens, 8 KV heads: 9.5 us
-// (lookups 1.5, one strip 1.8, the warps' merge 1, partials and their count 1, the last CTA's merge 2).
+// Measured on B200: all tokens of 8 sequences of 32-64K, 32/8 heads, bf16 out: 112 us, 4.0 TB/s of the
+// cache, 62% of the copy bandwidth (103 with one f16 for P); it is bound by the instructions that turn codes
+// into operands, not by memory or the MMAs.  Short launches are bound by their dependent steps: 64 blocks of
+// 64 tokens, 8 KV heads: 9.5 us (lookups 1.5, one strip 1.8, the warps' merge 1, partials and their count 1,
+// the last CTA's merge 2).
 #include <math.h>
 
 #include "common.cuh"
@@ -97,11 +97,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // An MMA drops what does not fit its accumulator instead of rounding it, so a long chain of them drifts
 // (fp32 outputs over 98K strips: 1.3e-6 off, and 7e-7 with the sums below; the plain fp32 form 4e-7).  For fp32 outputs a lane
 // therefore adds its accumulators to sums of its own in shared memory every kFlush strips.
-template <int NH, bool kSplitP>
+template <int NH, bool kF32>
 struct Layout {
-    static constexpr int kStages = kSplitP ? 2 : 3;
+    static constexpr int kStages = kF32 ? 2 : 3;
     static constexpr int kWarpRing = kStages * kStripBytes;
-    static constexpr int kSums = kSplitP ? NH * 32 * 32 * 4 : 0;  // per warp: [32 NH values][32 lanes]
+    static constexpr int kSums = kF32 ? NH * 32 * 32 * 4 : 0;  // per warp: [32 NH values][32 lanes]
     static constexpr int kBytes = kWarps * (kWarpRing + kSums);
 };
 
@@ -116,7 +116,7 @@ struct State {
     int lim[NH][2];     // tokens the row sees
 };
 
-template <int NH, bool kSplitP>
+template <int NH, bool kF32>
 __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)[NH][8][2], uint8_t* strip, int tok0,
                                              int valid, bool partial, int first_hidden, float* sums, int lane) {
     const int tr = lane >> 2, i = lane & 3;
@@ -229,7 +229,7 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
                     for (int mt = 0; mt < 8; ++mt) {
                         st.o[nh][mt][x] *= alpha;
                         st.o[nh][mt][2 + x] *= alpha;
-                        if (kSplitP) {  // (not in use, and not read, where the warp has fewer than kFlush strips)
+                        if (kF32) {  // (not in use, and not read, where the warp has fewer than kFlush strips)
                             sums[((nh * 8 + mt) * 4 + x) * 32] *= alpha;
                             sums[((nh * 8 + mt) * 4 + 2 + x) * 32] *= alpha;
                         }
@@ -254,10 +254,8 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
             for (int hh = 0; hh < 2; ++hh) {
                 const uint32_t hi = pack_f16(p[2 * hh], p[2 * hh + 1]);
                 ph[nh][mt][hh] = movmatrix_trans(hi);
-                if (kSplitP) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-                    pl[nh][mt][hh] = movmatrix_trans(pack_f16(p[2 * hh] - f.x, p[2 * hh + 1] - f.y));
-                }
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                pl[nh][mt][hh] = movmatrix_trans(pack_f16(p[2 * hh] - f.x, p[2 * hh + 1] - f.y));
             }
         }
     }
@@ -294,7 +292,7 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh) {
                     mma_f16_16816(st.o[nh][4 * w + m], a, ph[nh][mt][0], ph[nh][mt][1]);
-                    if (kSplitP) mma_f16_16816(st.o[nh][4 * w + m], a, pl[nh][mt][0], pl[nh][mt][1]);
+                    mma_f16_16816(st.o[nh][4 * w + m], a, pl[nh][mt][0], pl[nh][mt][1]);
                 }
             }
         }
@@ -338,9 +336,9 @@ __device__ __forceinline__ void move_sums(State<NH>& st, float* sums, bool back)
 
 // kShared: a CTA takes an equal share of all units' strips, which may span several units; else the grid
 // is (CTAs a unit, KV heads x row groups, sequences) and a CTA works on one unit.
-template <int NH, bool kSplitP, bool kShared>
+template <int NH, bool kF32, bool kShared>
 __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(Args a) {
-    using L = Layout<NH, kSplitP>;
+    using L = Layout<NH, kF32>;
     constexpr int R = 8 * NH, kStages = L::kStages;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint64_t full[kWarps][kStages];
@@ -503,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
         }
 
         const int first_hidden = len - a.M + 1;  // the first token that some row does not see
-        if (kSplitP && mine >= kFlush)
+        if (kF32 && mine >= kFlush)
 #pragma unroll
             for (int e = 0; e < NH * 32; ++e) sums[e * 32] = 0.f;
         for (int x = 0; x < mine; ++x) {
@@ -522,14 +520,14 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             }
             const int2 inf = info[warp][stage];
             if (inf.y != 0)
-                attend_strip<NH, kSplitP>(st, qb, my_ring + stage * kStripBytes, inf.x, abs(inf.y), inf.y < 0, first_hidden, sums, lane);
-            if (kSplitP && x % kFlush == kFlush - 1) move_sums(st, sums, false);
+                attend_strip<NH, kF32>(st, qb, my_ring + stage * kStripBytes, inf.x, abs(inf.y), inf.y < 0, first_hidden, sums, lane);
+            if (kF32 && x % kFlush == kFlush - 1) move_sums(st, sums, false);
             __syncwarp();
             if (x + kStages < mine) issue(x + kStages);
         }
 
         seq += mine;
-        if (kSplitP && mine >= kFlush) move_sums(st, sums, true);
+        if (kF32 && mine >= kFlush) move_sums(st, sums, true);
 
         // ---- merge the warps: each leaves its rows in its own ring ----
         float* mo = reinterpret_cast<float*>(my_ring);
@@ -714,11 +712,11 @@ Plan plan_of(const sba_cache4& c, int M, int n_max) {
     return p;
 }
 
-template <int NH, bool kSplitP, bool kShared>
+template <int NH, bool kF32, bool kShared>
 int launch_one(const Args& a, const Plan& p, cudaStream_t stream) {
-    if (allow_smem<decode_kv4_kernel<NH, kSplitP, kShared>>(Layout<NH, kSplitP>::kBytes) != SBA_OK) return SBA_ERR_CUDA;
+    if (allow_smem<decode_kv4_kernel<NH, kF32, kShared>>(Layout<NH, kF32>::kBytes) != SBA_OK) return SBA_ERR_CUDA;
     const dim3 grid = kShared ? dim3(p.ctas) : dim3(p.parts, a.H_kv * a.row_groups, a.B);
-    return launch(decode_kv4_kernel<NH, kSplitP, kShared>, grid, dim3(kThreads), Layout<NH, kSplitP>::kBytes, stream, a);
+    return launch(decode_kv4_kernel<NH, kF32, kShared>, grid, dim3(kThreads), Layout<NH, kF32>::kBytes, stream, a);
 }
 
 template <int NH>
