@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kFlush = 8;  // strips after which fp32 outputs move their sums out of the MMA accumulators
+constexpr int kFlush = 2;  // strips after which fp32 outputs move their sums out of the MMA accumulators
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMostParts = 128;           // CTAs a unit on average, at most: merging more takes longer than they save
@@ -94,9 +94,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
-// An MMA drops what does not fit its accumulator instead of rounding it, so a long chain of them drifts
-// (fp32 outputs over 98K strips: 1.3e-6 off, and 7e-7 with the sums below; the plain fp32 form 4e-7).  For fp32 outputs a lane
-// therefore adds its accumulators to sums of its own in shared memory every kFlush strips.
+// An MMA drops what does not fit its accumulator instead of rounding it, so a long chain of them drifts.  For
+// fp32 outputs a lane therefore adds its accumulators to sums of its own in shared memory every kFlush strips.
+// Error and time over all tokens of 8 sequences of 32-64K, by kFlush: never 1.3e-6; 8: 7.4e-7, 116 us; 4:
+// 4.7e-7, 118; 2: 3.6e-7, 121; 1: 3.2e-7, 129.  The plain fp32 form is 3.9e-7 off.
 template <int NH, bool kF32>
 struct Layout {
     static constexpr int kStages = kF32 ? 2 : 3;

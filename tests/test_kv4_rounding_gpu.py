@@ -60,3 +60,39 @@ def test_bf16_outputs_are_the_fp32_result_rounded_once(b, G, M, T):
         lo, hi = rounded(o - tol), rounded(o + tol)
         assert ((lo <= g) & (g <= hi)).all(), (h, int(((g < lo) | (g > hi)).sum()), g.size)
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("H,G", [(8, 1), (4, 16)])
+def test_fp32_sums_over_many_strips_are_rounded_not_cut(H, G):
+    """Equal weights (a query of zeros: P is 2^8 and the sum of 2048 of them a power of two, all exact) and
+    values of 7168 and of 1 or 3 times u = 2^-6, in every eighth strip only: one warp has them all, eight
+    strips, and every other warp adds zeros.  16 tokens (an MMA step) hold nine large values and seven small
+    ones, so two strips add up to less than 2^24 u: exact in an accumulator.  The sums of two strips are then
+    added by rounding, to values below 2^25 u, 1.5 * 2^25 u and 2^26 u: at most 1 + 2 + 2 u off.  An
+    accumulator that runs through all eight strips passes 2^24 u after the second, and every step (an odd
+    number of u) is cut by 1 u or more: 4 steps in strips 3 and 4, 8 in strips 5 to 8, at least 12 u."""
+    b, B, T = 64, 37, 2048                                    # a unit a CTA: 296 of 8 rows, 148 of 16
+    lay = layout([T] * B, b, False, 0, slack=0)
+    g = torch.Generator().manual_seed(G)
+    kv = torch.zeros((lay.pages, H, b // 32, 4608), dtype=torch.uint8)
+    sums = np.zeros((B, H, 128))
+    big = torch.zeros(16, dtype=torch.bool)
+    big[[0, 1, 3, 5, 6, 8, 10, 11, 15]] = True
+    for x in range(8):
+        page, strip = 8 * x // 2, 8 * x % 2                   # strip 8x of every sequence
+        three = torch.randint(0, 2, (B, H, 32, 128), generator=g).bool()
+        large = big.repeat(2)[:, None].expand(B, H, 32, 128)
+        code = torch.where(large, 6, torch.where(three, 5, 2)).to(torch.uint8)       # 4, 3, 1
+        scale = torch.where(large[..., ::16], 206, 72).to(torch.uint8)               # 1792, 2^-6
+        at = torch.arange(B) * (T // b) + page
+        kv[at, :, strip, 2048:4096] = (code[..., 0::2] | (code[..., 1::2] << 4)).reshape(B, H, 2048)
+        kv[at, :, strip, 4352:4608] = scale.reshape(B, H, 256)
+        sums += torch.where(large, 7168.0, torch.where(three, 3.0, 1.0) / 64).double().sum(2).numpy()
+    c = cache4(lay, kv, H_q=H * G, desc=False)
+    q = torch.zeros((B, H * G, 128), dtype=torch.bfloat16, device=DEV)
+    out = torch.empty((B, H * G, 128), dtype=torch.float32, device=DEV)
+    ws = torch.zeros(sba.sba_decode_kv4_workspace_size(c, 1, 0), dtype=torch.uint8, device=DEV)
+    sba.sba_decode_kv4(c, q, 1.0, out, ws)
+    off = np.abs(f64(out).reshape(B, H, G, 128) * T - sums[:, :, None]) * 64
+    assert off.max() <= 5, off.max()
+    assert int(c.status.item()) == 0
