@@ -353,7 +353,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     }
     if (warp == 0) tc::alloc(&tmem_at, kTcCols);
     pdl_wait();
-    pdl_trigger();
 
     // ---- this CTA's share: an equal part of all the units' tiles, whatever their lengths.  A tile is four
     // strips, a unit one (sequence, KV head) ----
@@ -373,6 +372,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
+    pdl_trigger();  // not before this CTA holds its tensor memory: the next kernel's CTAs may want some too
     const uint32_t uwarp = tc::uniform(warp), group = uwarp >> 2;
     const uint32_t tm = tc::uniform(tmem_at) + group * kTcGroupCols, my_lanes = (uint32_t)(32 * (uwarp & 3)) << 16;
     const bool issuer = (uwarp & 3) == 0;  // the group's warp that issues its products

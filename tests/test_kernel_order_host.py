@@ -1,0 +1,28 @@
+"""Orders in the kernel sources that no run can show safely: what would go wrong is a GPU that hangs."""
+from __future__ import annotations
+
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_sparse_gqa_min_b200", "csrc")
+
+
+def code(name: str) -> str:
+    """A source file without its comments."""
+    text = open(os.path.join(CSRC, name)).read()
+    return re.sub(r"//[^\n]*", "", re.sub(r"/\*.*?\*/", "", text, flags=re.S))
+
+
+def test_the_next_kernel_starts_after_tensor_memory_is_held():
+    """A CTA that lets the next kernel start before it holds its tensor memory can lose it to that kernel's
+    CTA on the same SM, which keeps it while it waits for this one.  One thread's launch_dependents counts for
+    its CTA, so a barrier has to lie between the allocation and any thread's trigger."""
+    seen = 0
+    for part in code("weights.cu").split("__global__")[1:]:
+        if "tc::alloc(" not in part:
+            continue
+        seen += 1
+        between = part[part.index("tc::alloc("):part.index("pdl_trigger()")]
+        assert part.index("pdl_trigger()") > part.index("tc::alloc(")
+        assert "__syncthreads()" in between
+    assert seen == 1
