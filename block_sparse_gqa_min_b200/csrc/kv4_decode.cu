@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
     uint8_t* my_ring = ring + warp * L::kWarpRing;
     float* sums = reinterpret_cast<float*>(ring + kWarps * L::kWarpRing + warp * L::kSums) + lane;
     int seq = 0;        // strips this warp has been through (their stages and phases)
-    bool alive = true;  // no wait of this warp has run out
+    bool alive = true;  // no wait of this warp has run out (the same in all lanes)
 
     int64_t base = kShared ? share.start - share.at : 0;  // first strip of the unit, among all units'
     int left = kShared ? share.left : 1, at = kShared ? share.at : 0, unit = kShared ? share.unit : 0;
@@ -507,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             for (int e = 0; e < NH * 32; ++e) sums[e * 32] = 0.f;
         for (int x = 0; x < mine; ++x) {
             const int stage = (seq + x) % kStages;
-            if (!mbar_wait(&full[warp][stage], ((seq + x) / kStages) & 1, a.status)) {
+            if (!mbar_wait_warp(&full[warp][stage], ((seq + x) / kStages) & 1, a.status)) {
                 // give up: nothing of this warp enters the merge, and its copies in flight get the same limit again
                 for (int y = seq + x; y < seq + min(mine, x + kStages); ++y)
-                    mbar_wait(&full[warp][y % kStages], (y / kStages) & 1, a.status);
+                    mbar_wait_warp(&full[warp][y % kStages], (y / kStages) & 1, a.status);
                 alive = false;
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh) {

@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                     // every thread of the group has stored its keys and read its logits of the chunk before
                     tc::fence_before();
                     asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
-                    if (issuer && __all_sync(0xffffffffu, alive)) {
+                    if (issuer && alive) {
                         tc::fence_after();
                         const uint32_t id = tc::idesc(128, n, !kFour), step = (uint32_t)c0 * 128 >> 4;
                         if (tc::elect()) {
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
                         }
                         __syncwarp();
                     }
-                    // a wait that ran out leaves the thread to the barriers only
-                    if (alive) alive = mbar_wait(&done[group], phase, a.status);
+                    // a wait that ran out leaves the warp to the barriers only
+                    if (alive) alive = mbar_wait_warp(&done[group], phase, a.status);
                     phase ^= 1;
                     tc::fence_after();
                     const bool all_seen = chunk_plain[c0 / kTcChunk] && __all_sync(0xffffffffu, this_tok < first_hidden);
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) accumulate_weights_tc_kernel(Ar
             }
         }
     }
-    if (!alive && issuer) mbar_wait(&done[group], phase ^ 1, a.status);  // products still in flight
+    if (!alive && issuer) mbar_wait_warp(&done[group], phase ^ 1, a.status);  // products still in flight
     tc::fence_before();
     __syncthreads();
     if (warp == 0) {

@@ -141,6 +141,7 @@ _SIGS = {
     "sba_fold_gate": ([ctypes.POINTER(sba_gate), _P, _P], ctypes.c_int),
     "sba_static_scratch_bytes": ([], ctypes.c_size_t),
     "sba_selftest_wait_timeout": ([_P, ctypes.c_uint64, _P], ctypes.c_int),
+    "sba_selftest_wait_vote": ([_P, _P, ctypes.c_uint64, _P], ctypes.c_int),
     "sba_score_select_static": ([ctypes.POINTER(sba_cache), _P, ctypes.POINTER(sba_select_params), _P, _P, _P, _I,
                                  _P], ctypes.c_int),
     "sba_decode_step_cluster": ([ctypes.POINTER(sba_cache), ctypes.POINTER(sba_select_params)], _I),
@@ -389,6 +390,15 @@ def sba_selftest_wait_timeout(status: torch.Tensor, limit_ns: int, stream=None):
     is OR-ed into the int32 device `status`, the kernel returns."""
     _check(load().sba_selftest_wait_timeout(_ptr(status), int(limit_ns), _stream(stream)),
            "sba_selftest_wait_timeout")
+
+
+def sba_selftest_wait_vote(status: torch.Tensor, verdicts: torch.Tensor, limit_ns: int, stream=None):
+    """Let a wait of a whole warp run out for half of its lanes: int32 device `verdicts` [32] gets 0 for
+    every lane, SBA_DEV_TIMEOUT is OR-ed into `status`."""
+    dev = verdicts.get_device()
+    _check(load().sba_selftest_wait_vote(_tensor(status, torch.int32, dev, 1, "status"),
+                                         _tensor(verdicts, torch.int32, dev, 32, "verdicts"), int(limit_ns),
+                                         _stream(stream)), "sba_selftest_wait_vote")
 
 
 def sba_decode_step_cluster(c: Cache, p: sba_select_params) -> int:

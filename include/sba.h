@@ -207,6 +207,12 @@ const char *sba_last_cuda_error(void);
  * for a NULL status).  The kernels' own waits give up after about 2 s. */
 int sba_selftest_wait_timeout(int32_t *status, uint64_t limit_ns, void *stream);
 
+/* Self-test of the wait that a whole warp makes: the lanes of one warp wait on one barrier, half of them
+ * limited to limit_ns and half to four times that, and the barrier completes after twice limit_ns.  A warp
+ * gives up as one: verdicts (device int32 [32]) gets 0 for every lane, and SBA_DEV_TIMEOUT is ORed into
+ * *status.  0 < limit_ns <= 1 s (SBA_ERR_INVALID_ARG otherwise, or for a NULL pointer). */
+int sba_selftest_wait_vote(int32_t *status, int32_t *verdicts, uint64_t limit_ns, void *stream);
+
 /* Host helper: blocks selected for a sequence of N blocks under `p` (the rule
  * above).  Returns -1 if p is NULL. */
 int32_t sba_num_selected(int32_t N, const sba_select_params *p);

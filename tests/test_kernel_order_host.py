@@ -26,3 +26,21 @@ def test_the_next_kernel_starts_after_tensor_memory_is_held():
         assert part.index("pdl_trigger()") > part.index("tc::alloc(")
         assert "__syncthreads()" in between
     assert seen == 1
+
+
+def test_waits_before_full_warp_operations_have_one_verdict():
+    """The four-bit attention and the tensor-memory weights go on with full-mask shuffles and warp-wide MMAs
+    after a wait, so all lanes have to give up together or not at all."""
+    for name in ("kv4_decode.cu", "weights.cu"):
+        text = code(name)
+        assert re.findall(r"\bmbar_wait_warp\(", text), name
+        assert not re.findall(r"\bmbar_wait\(|\bmbar_wait_sleep\(", text), name
+
+
+def test_bad_arguments_of_the_warp_wait_test():
+    from block_sparse_gqa_min_b200 import sba
+
+    call = sba.load().sba_selftest_wait_vote
+    for status, verdicts, limit in ((None, 0x1000, 1000), (0x1000, None, 1000), (0x1000, 0x2000, 0),
+                                    (0x1000, 0x2000, 1_000_000_001)):
+        assert call(status, verdicts, limit, None) == sba.SBA_ERR_INVALID_ARG
