@@ -175,7 +175,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs
         }
     }
 #pragma unroll 2
-    for (int i = tid + (held - tid + kSelThreads - 1) / kSelThreads * kSelThreads; i < nq; i += kSelThreads) count(quad(i));
+    for (int i = tid + (held - tid + kSelThreads - 1) / kSelThreads * kSelThreads; i < nq; i += kSelThreads) {
+        const int at = cell_of(i);
+        if (at < 0) report(a.status, SBA_DEV_BAD_PAGE);  // here once; the later passes look at it again
+        count(keys_of(i, weights_of(at)));
+    }
     __syncthreads();
     if (tid < kBins) {
         uint32_t c = 0;
