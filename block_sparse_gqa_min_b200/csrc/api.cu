@@ -358,6 +358,12 @@ int check_weights(const float* lse, const float* acc_in, const float* acc_out) {
     return SBA_OK;
 }
 
+size_t cells(const sba_cache& c) { return (size_t)c.num_pages * c.H_kv * c.b; }
+bool overlap(const float* x, size_t nx, const float* y, size_t ny) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return x && y && a < b + ny * 4 && b < a + nx * 4;
+}
+
 // Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before).
 int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* p, const sba_cache& dst,
                 const float* acc_dst, const int32_t* new_lens, const int32_t* kept) {
@@ -366,12 +372,17 @@ int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* 
         return SBA_ERR_INVALID_ARG;
     if (dst.B != src.B || dst.H_kv != src.H_kv || dst.b != src.b) return SBA_ERR_INVALID_ARG;
     if ((int64_t)p->n_keep > (int64_t)dst.max_blocks * dst.b) return SBA_ERR_INVALID_ARG;
-    // the lengths are read while the new ones are written, the rows while others are
+    // the lengths are read while the new ones are written
     const intptr_t apart = reinterpret_cast<intptr_t>(new_lens) - reinterpret_cast<intptr_t>(src.seq_lens);
     const intptr_t size = (intptr_t)src.B * 4;
-    if ((apart > -size && apart < size) || acc_dst == acc || (dst.desc && dst.desc == src.desc && !dst.block_table))
-        return SBA_ERR_INVALID_ARG;
-    if ((dst.k == src.k || dst.v == src.v) && !dst.block_table && !src.block_table) return SBA_ERR_INVALID_ARG;
+    if (apart > -size && apart < size) return SBA_ERR_INVALID_ARG;
+    // One pool: the caches' pages are apart only where a block table says so, for without one either begins at
+    // page 0.  Its weights are one array too; weights of different pools, or that overlap in any other way, are
+    // read where others are written.
+    const bool one_pool = dst.k == src.k && dst.v == src.v;
+    if (!src.block_table && !dst.block_table && (dst.k == src.k || dst.v == src.v)) return SBA_ERR_INVALID_ARG;
+    if (dst.desc && dst.desc == src.desc && !dst.block_table && !(one_pool && src.block_table)) return SBA_ERR_INVALID_ARG;
+    if (acc_dst == acc ? !one_pool : overlap(acc, cells(src), acc_dst, cells(dst))) return SBA_ERR_INVALID_ARG;
     if (src.B > 65535 || src.H_kv > 65535) return SBA_ERR_UNSUPPORTED;
     return SBA_OK;
 }

@@ -495,6 +495,7 @@ int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t 
  *               is -inf adds nothing.
  * gate_bias     as sba_sparse_decode (fp32 [B][H_q][n_max]), or NULL; needs a selection and M = 1.
  * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); may be the same.
+ * A token that has just been appended needs acc_in 0 in its cells: no call clears them.
  * A selection lists every block once, ascending; an entry that is not larger than the one before it is
  * skipped and reports SBA_DEV_BAD_SELECTION (what a list that still names a block twice adds to that
  * block is not defined).  No atomics: the same inputs give the same bits. */
@@ -515,7 +516,10 @@ int sba_accumulate_weights_kv4(const sba_cache4 *c, const void *q, int32_t M, co
  *            read (new_lens is a good value for it).  dst->desc, when non-NULL, receives the Quest
  *            descriptors of the blocks written; gate keys are not refreshed (call
  *            sba_update_descriptors for them).  Rows of dst past the kept ones are left as they were.
- * acc_dst    device fp32 [dst->num_pages][H_kv][b] or NULL: the kept tokens' weights; not acc itself.
+ * acc_dst    device fp32 [dst->num_pages][H_kv][b] or NULL: the kept tokens' weights.  Where src and dst share
+ *            their rows' pool, acc itself is a good value; otherwise it does not overlap acc.  Cells past the
+ *            kept tokens are left as they were: the caller sets a token's cells to 0 when it appends the
+ *            token (pages that are used again hold their last tokens' weights).
  * new_lens   device int32 [B]: min(len_s, n_keep); does not overlap src->seq_lens.
  * kept       device int32 [B][H_kv][n_keep]: the kept positions in src, ascending; entries past the
  *            new length are left as they were. */
