@@ -624,8 +624,9 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     // pays for the longer start: four bits, 16K tokens: 16 rows 8.3 against 8.2, 32 rows 10.7 against 9.2; 4K
     // tokens: 32 rows 5.9 against 6.4, 64 rows 8.2 against 7.6; bf16, 16K tokens: 32 rows 11.7 against 13.2,
     // 64 rows 16.2 against 15.2.
+    // Gated calls (one token: at most 16 rows) stay with the first kernel, the one that takes a bias.
     const int least = few ? (kFour ? 24 : 64) : (kFour ? 1 : 24);
-    if (a.rows >= least) {
+    if (!gate_bias && a.rows >= least) {
         // every CTA that fits (two an SM) once, and at least one tile a warpgroup
         const int64_t wide = (blocks * (c.b / kStripTokens) + 3) / 4, groups = (wide * units + kTcGroups - 1) / kTcGroups;
         if (allow_smem<accumulate_weights_tc_kernel<kFour>>(kTcSmem) != SBA_OK) return SBA_ERR_CUDA;
@@ -637,7 +638,8 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
         return launch(accumulate_weights_kernel<kFour, false>, dim3((unsigned)(x < 1 ? 1 : x), c.H_kv, c.B), dim3(kThreads), 0,
                       stream, a);
     }
-    if constexpr (kFour) return SBA_OK;  // (taken by the tensor-memory kernel above)
+    // (long four-bit launches have all been taken above, and have no instance here)
+    if constexpr (kFour) return SBA_ERR_UNSUPPORTED;
     else return launch(accumulate_weights_kernel<false, true>, dim3((unsigned)fit), dim3(kThreads), 0, stream, a);
 }
 

@@ -44,3 +44,15 @@ def test_bad_arguments_of_the_warp_wait_test():
     for status, verdicts, limit in ((None, 0x1000, 1000), (0x1000, None, 1000), (0x1000, 0x2000, 0),
                                     (0x1000, 0x2000, 1_000_000_001)):
         assert call(status, verdicts, limit, None) == sba.SBA_ERR_INVALID_ARG
+
+
+def test_a_weights_call_that_says_ok_has_launched():
+    """Whatever the thresholds between the two kernels are: no way through the dispatch returns SBA_OK by
+    itself, and a call with a gate bias never goes to the kernel that takes none."""
+    text = code("weights.cu")
+    dispatch = text[text.index("int launch_weights("):]
+    dispatch = dispatch[:dispatch.index("\n}\n")]
+    assert "return SBA_OK" not in dispatch
+    conditions = re.findall(r"if \(([^{]*a\.rows >= least)\) \{", dispatch)
+    assert conditions == ["!gate_bias && a.rows >= least"]
+    assert "gate_bias" not in text[text.index("void __launch_bounds__(kTcThreads, 2)"):text.index("int launch_weights(")]
