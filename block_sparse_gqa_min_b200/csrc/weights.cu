@@ -29,7 +29,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileTokens = 16;
-constexpr int kRowTiles = 16;  // row tiles of 8 staged at a time (128 rows, 32 KB)
+constexpr int kRowTiles = 8;  // row tiles of 8, all staged at once: 64 rows, 16 KB (more go to the second kernel)
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Args {
@@ -179,115 +179,112 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
             if (page >= 0 && tok < len) row = (page * a.H_kv + h) * a.b + (g % tpb) * kTileTokens;
         };
 
-        for (int r0 = 0; r0 < a.rows; r0 += kRowTiles * 8) {
-            const int n_rows = min(kRowTiles * 8, a.rows - r0), n_tiles = (n_rows + 7) / 8;
-            // ---- the rows' operand fragments, scales, lse and limits ----
-            if (kShared || r0) __syncthreads();  // the rows before are done with
-            for (int t = warp; t < n_tiles; t += kWarps) {
-                const int r = r0 + t * 8 + tr;
-                const bool real = r < a.rows;
-                const int64_t qrow = real ? ((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G : 0;
-                const __nv_bfloat16* p = a.q + qrow * kHeadDim;
-                uint32_t w[8][2];
-                float mx = 0.f;
+        const int n_tiles = (a.rows + 7) / 8;
+        // ---- the rows' operand fragments, scales, lse and limits ----
+        if (kShared) __syncthreads();  // the unit before is done with its rows
+        for (int t = warp; t < n_tiles; t += kWarps) {
+            const int r = t * 8 + tr;
+            const bool real = r < a.rows;
+            const int64_t qrow = real ? ((int64_t)s * a.M + r / G) * a.H_q + h * G + r % G : 0;
+            const __nv_bfloat16* p = a.q + qrow * kHeadDim;
+            uint32_t w[8][2];
+            float mx = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t v =
+                        real ? __ldca(reinterpret_cast<const uint32_t*>(p + Keys<kFour>::channel(ks, qi, half))) : 0u;
+                    w[ks][half] = v;
+                    mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(v)), fabsf(bf16_hi(v))));
+                }
+            float up = 1.f;
+            if (kFour) {  // f16 operands: the row scaled by a power of two to a maximum in [1, 2)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const int e = row_exponent(mx);
+                const float down = pow2(-e);
+                up = pow2(e);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const uint32_t v =
-                            real ? __ldca(reinterpret_cast<const uint32_t*>(p + Keys<kFour>::channel(ks, qi, half))) : 0u;
-                        w[ks][half] = v;
-                        mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(v)), fabsf(bf16_hi(v))));
-                    }
-                float up = 1.f;
-                if (kFour) {  // f16 operands: the row scaled by a power of two to a maximum in [1, 2)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const int e = row_exponent(mx);
-                    const float down = pow2(-e);
-                    up = pow2(e);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half)
-                            w[ks][half] = pack_f16(bf16_lo(w[ks][half]) * down, bf16_hi(w[ks][half]) * down);
-                }
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) qf[t][ks][lane] = make_uint2(w[ks][0], w[ks][1]);
-                const float lse = real ? __ldca(a.lse + qrow) : -INFINITY;
-                const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
-                if (qi == 0) {
-                    row_sc[t * 8 + tr] = a.scale_log2 * up;
-                    row_lse[t * 8 + tr] = counts ? lse * kLog2e : 0.f;
-                    row_lim[t * 8 + tr] = counts ? len - a.M + r / G + 1 : 0;
-                }
-                const int all = __all_sync(0xffffffffu, counts);
-                if (lane == 0) tile_plain[t] = all;
+                    for (int half = 0; half < 2; ++half)
+                        w[ks][half] = pack_f16(bf16_lo(w[ks][half]) * down, bf16_hi(w[ks][half]) * down);
             }
-            __syncthreads();
-
-            const float* acc_from = r0 ? a.acc_out : a.acc_in;
-            const int first_hidden = len - a.M + 1;
-            Keys<kFour> next;
-            auto fetch = [&](int x) {
-                if ((x & 31) == 0) resolve(x + lane);
-                const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
-                if (from >= 0) next.load(a.k, from, lane);
-            };
-            int64_t cur_row = -1;
-            int cur_tok = 0, cur_pos = 0;
-            if (mine > 0) fetch(0);
-            for (int x = 0; x < mine; ++x) {
-                cur_row = __shfl_sync(0xffffffffu, row, x & 31);
-                cur_tok = __shfl_sync(0xffffffffu, tok, x & 31);
-                cur_pos = __shfl_sync(0xffffffffu, pos, x & 31);
-                uint32_t kf[8][4];
-                next.operand(kf);
-                if (x + 1 < mine) fetch(x + 1);
-                if (cur_row < 0) continue;
-                float w0 = 0.f, w1 = 0.f;
-                const bool all_seen = cur_tok + kTileTokens <= first_hidden;
-                for (int t = 0; t < n_tiles; ++t) {
-                    float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int ks = 0; ks < 8; ks += 2) {
-                        const uint2 b0 = qf[t][ks][lane], b1 = qf[t][ks + 1][lane];
-                        if (kFour) {
-                            mma_f16_16816(e, kf[ks], b0.x, b0.y);
-                            mma_f16_16816(o, kf[ks + 1], b1.x, b1.y);
-                        } else {
-                            mma_bf16_16816(e, kf[ks], b0.x, b0.y);
-                            mma_bf16_16816(o, kf[ks + 1], b1.x, b1.y);
-                        }
+            for (int ks = 0; ks < 8; ++ks) qf[t][ks][lane] = make_uint2(w[ks][0], w[ks][1]);
+            const float lse = real ? __ldca(a.lse + qrow) : -INFINITY;
+            const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
+            if (qi == 0) {
+                row_sc[t * 8 + tr] = a.scale_log2 * up;
+                row_lse[t * 8 + tr] = counts ? lse * kLog2e : 0.f;
+                row_lim[t * 8 + tr] = counts ? len - a.M + r / G + 1 : 0;
+            }
+            const int all = __all_sync(0xffffffffu, counts);
+            if (lane == 0) tile_plain[t] = all;
+        }
+        __syncthreads();
+
+        const int first_hidden = len - a.M + 1;
+        Keys<kFour> next;
+        auto fetch = [&](int x) {
+            if ((x & 31) == 0) resolve(x + lane);
+            const int64_t from = __shfl_sync(0xffffffffu, row, x & 31);
+            if (from >= 0) next.load(a.k, from, lane);
+        };
+        int64_t cur_row = -1;
+        int cur_tok = 0, cur_pos = 0;
+        if (mine > 0) fetch(0);
+        for (int x = 0; x < mine; ++x) {
+            cur_row = __shfl_sync(0xffffffffu, row, x & 31);
+            cur_tok = __shfl_sync(0xffffffffu, tok, x & 31);
+            cur_pos = __shfl_sync(0xffffffffu, pos, x & 31);
+            uint32_t kf[8][4];
+            next.operand(kf);
+            if (x + 1 < mine) fetch(x + 1);
+            if (cur_row < 0) continue;
+            float w0 = 0.f, w1 = 0.f;
+            const bool all_seen = cur_tok + kTileTokens <= first_hidden;
+            for (int t = 0; t < n_tiles; ++t) {
+                float e[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < 8; ks += 2) {
+                    const uint2 b0 = qf[t][ks][lane], b1 = qf[t][ks + 1][lane];
+                    if (kFour) {
+                        mma_f16_16816(e, kf[ks], b0.x, b0.y);
+                        mma_f16_16816(o, kf[ks + 1], b1.x, b1.y);
+                    } else {
+                        mma_bf16_16816(e, kf[ks], b0.x, b0.y);
+                        mma_bf16_16816(o, kf[ks + 1], b1.x, b1.y);
                     }
-                    const int r = t * 8 + 2 * qi;
-                    const float2 sc = *reinterpret_cast<const float2*>(&row_sc[r]);
-                    float2 off = *reinterpret_cast<const float2*>(&row_lse[r]);
-                    if (a.gate_bias) {
-                        const int64_t at = ((int64_t)s * a.H_q + h * G + r0 + r) * a.n_max + cur_pos;
-                        if (r0 + r < a.rows) off.x -= __ldca(a.gate_bias + at) * kLog2e;
-                        if (r0 + r + 1 < a.rows) off.y -= __ldca(a.gate_bias + at + a.n_max) * kLog2e;
-                    }
-                    float p0 = ex2(fmaf(e[0] + o[0], sc.x, -off.x)), p1 = ex2(fmaf(e[1] + o[1], sc.y, -off.y));
-                    float p2 = ex2(fmaf(e[2] + o[2], sc.x, -off.x)), p3 = ex2(fmaf(e[3] + o[3], sc.y, -off.y));
-                    if (!all_seen || !tile_plain[t]) {
-                        const int2 lim = *reinterpret_cast<const int2*>(&row_lim[r]);
-                        if (cur_tok + tr >= lim.x) p0 = 0.f;
-                        if (cur_tok + tr >= lim.y) p1 = 0.f;
-                        if (cur_tok + tr + 8 >= lim.x) p2 = 0.f;
-                        if (cur_tok + tr + 8 >= lim.y) p3 = 0.f;
-                    }
-                    w0 += p0 + p1;
-                    w1 += p2 + p3;
                 }
-                w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
-                w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
-                w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
-                w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-                if (qi < 2) {  // lane 0 of a quad writes token tr, lane 1 token tr + 8
-                    const int t = tr + 8 * qi;
-                    if (cur_tok + t < len) a.acc_out[cur_row + t] = acc_from[cur_row + t] + (qi ? w1 : w0);
+                const int r = t * 8 + 2 * qi;
+                const float2 sc = *reinterpret_cast<const float2*>(&row_sc[r]);
+                float2 off = *reinterpret_cast<const float2*>(&row_lse[r]);
+                if (a.gate_bias) {
+                    const int64_t at = ((int64_t)s * a.H_q + h * G + r) * a.n_max + cur_pos;
+                    if (r < a.rows) off.x -= __ldca(a.gate_bias + at) * kLog2e;
+                    if (r + 1 < a.rows) off.y -= __ldca(a.gate_bias + at + a.n_max) * kLog2e;
                 }
+                float p0 = ex2(fmaf(e[0] + o[0], sc.x, -off.x)), p1 = ex2(fmaf(e[1] + o[1], sc.y, -off.y));
+                float p2 = ex2(fmaf(e[2] + o[2], sc.x, -off.x)), p3 = ex2(fmaf(e[3] + o[3], sc.y, -off.y));
+                if (!all_seen || !tile_plain[t]) {
+                    const int2 lim = *reinterpret_cast<const int2*>(&row_lim[r]);
+                    if (cur_tok + tr >= lim.x) p0 = 0.f;
+                    if (cur_tok + tr >= lim.y) p1 = 0.f;
+                    if (cur_tok + tr + 8 >= lim.x) p2 = 0.f;
+                    if (cur_tok + tr + 8 >= lim.y) p3 = 0.f;
+                }
+                w0 += p0 + p1;
+                w1 += p2 + p3;
+            }
+            w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
+            w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
+            w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
+            w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
+            if (qi < 2) {  // lane 0 of a quad writes token tr, lane 1 token tr + 8
+                const int t = tr + 8 * qi;
+                if (cur_tok + t < len) a.acc_out[cur_row + t] = a.acc_in[cur_row + t] + (qi ? w1 : w0);
             }
         }
         if constexpr (!kShared) return;
@@ -625,7 +622,8 @@ int launch_weights(const Cache& c, const void* keys, const void* q, int M, const
     // tokens: 32 rows 5.9 against 6.4, 64 rows 8.2 against 7.6; bf16, 16K tokens: 32 rows 11.7 against 13.2,
     // 64 rows 16.2 against 15.2.
     // Gated calls (one token: at most 16 rows) stay with the first kernel, the one that takes a bias.
-    const int least = few ? (kFour ? 24 : 64) : (kFour ? 1 : 24);
+    static_assert(kMaxGroup <= kRowTiles * 8, "a gated call's rows fit");
+    const int least = few ? (kFour ? 24 : kRowTiles * 8) : (kFour ? 1 : 24);
     if (!gate_bias && a.rows >= least) {
         // every CTA that fits (two an SM) once, and at least one tile a warpgroup
         const int64_t wide = (blocks * (c.b / kStripTokens) + 3) / 4, groups = (wide * units + kTcGroups - 1) / kTcGroups;
