@@ -493,7 +493,10 @@ int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t 
  * acc_out of other tokens is left as it was.
  * lse           device fp32 [B][M][H_q], as the attention of the same step returned it; a row whose lse
  *               is -inf adds nothing.
- * gate_bias     as sba_sparse_decode (fp32 [B][H_q][n_max]), or NULL; needs a selection and M = 1.
+ * gate_bias     as sba_sparse_decode (fp32 [B][H_q][n_max]), or NULL; needs a selection and M = 1.  The log
+ *               gates of an attention that has them in its logits (inner: the rows' weights sum to 1) or
+ *               on its values (outer: lse is that of the ungated logits, so the sum is what each value
+ *               entered the output with, gate included); NULL where the gate only selects.
  * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); may be the same.
  * A token that has just been appended needs acc_in 0 in its cells: no call clears them.
  * A selection lists every block once, ascending; an entry that is not larger than the one before it is
