@@ -117,9 +117,11 @@ __device__ __forceinline__ void mma_f16_16816(float* d, const uint32_t* a, uint3
 }
 
 // Power of two that brings a row whose largest magnitude is mx to a maximum in [1, 2), as its
-// exponent e (x * 2^-e); rows of zeros, infinities and NaN get one that changes nothing else.
+// exponent e (x * 2^-e), within the exponents whose powers and reciprocals are normal numbers: a row of the
+// largest bf16 values comes to [2, 4), one of the smallest subnormals to 2^-7 and more.  Rows of zeros,
+// infinities and NaN get one that changes nothing else.
 __device__ __forceinline__ int row_exponent(float mx) {
-    return max(-100, min(100, (int)(__float_as_uint(mx) >> 23) - 127));
+    return max(-126, min(126, (int)(__float_as_uint(mx) >> 23) - 127));
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 

@@ -30,6 +30,7 @@
 // into operands, not by memory or the MMAs.  Short launches are bound by their dependent steps: 64 blocks of
 // 64 tokens, 8 KV heads: 9.5 us (lookups 1.5, one strip 1.8, the warps' merge 1, partials and their count 1,
 // the last CTA's merge 2).
+#include <float.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -492,7 +493,9 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
             for (int x = 0; x < 2; ++x) {
                 const int re = __shfl_sync(0xffffffffu, e, (2 * qi + x) * 4);
                 const int rr = rg * R + nh * 8 + 2 * qi + x;
-                st.sc[nh][x] = a.scale_log2 * pow2(re);
+                // (a normal number: 0 would make a NaN of the first maximum, -inf, and of what is masked, and infinity
+                // one of the maximum itself; logits so small are all alike, and so large one apart)
+                st.sc[nh][x] = fminf(fmaxf(a.scale_log2 * pow2(re), FLT_MIN), FLT_MAX);
                 st.lim[nh][x] = rr < a.rows ? len - a.M + rr / G + 1 : 0;
                 st.m[nh][x] = st.high[nh][x] = -INFINITY;
                 st.l[nh][x] = 0.f;

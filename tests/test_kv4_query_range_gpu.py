@@ -1,0 +1,71 @@
+"""Four-bit attention and weights for queries and scales at the ends of their ranges: a power of two moved from
+the scale to the query changes no bit, and rows whose logits vanish weigh all tokens alike."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from block_sparse_gqa_min_b200 import sba
+from oracle import small_cache as SC
+from tests.kv4_helpers import SCALE, cache4, f64, layout, packed, rand_bf16
+from tests.test_kv4_gpu import i32
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+DEV = torch.device("cuda")
+
+
+def run(c, q, scale):
+    B, M, HQ, _ = q.shape
+    out, lse = torch.empty(q.shape, device=DEV), torch.empty((B, M, HQ), device=DEV)
+    ws = torch.zeros(sba.sba_decode_kv4_workspace_size(c, M, 0), dtype=torch.uint8, device=DEV)
+    sba.sba_decode_kv4(c, q.to(DEV), scale, out, ws, lse_out=lse)
+    acc = torch.zeros((c.num_pages, c.H_kv, c.b), device=DEV)
+    sba.sba_accumulate_weights_kv4(c, q.to(DEV), lse, scale, acc, acc)
+    return out, lse, acc
+
+
+def cache(lens, H, G):
+    lay = layout(lens, 64, False, 0)
+    k, v = rand_bf16((lay.pages, H, 64, 128), 1), rand_bf16((lay.pages, H, 64, 128), 2)
+    kv = packed(k, v)
+    return lay, kv, cache4(lay, kv, H_q=H * G, desc=False)
+
+
+@pytest.mark.parametrize("G,M", [(4, 1), (8, 4)])              # 4 rows, and 32: the register and the tensor-memory weights
+@pytest.mark.parametrize("e", [124, 110, -110])
+def test_a_power_of_two_of_the_query_is_one_of_the_scale(G, M, e):
+    lay, kv, c = cache([1000, 70], 2, G)
+    q = rand_bf16((2, M, 2 * G, 128), 3, 0)
+    moved = (q.double() * 2.0 ** e).to(torch.bfloat16)
+    assert torch.equal(moved.double() * 2.0 ** -e, q.double())
+    want, got = run(c, q, SCALE), run(c, moved, SCALE * 2.0 ** -e)
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+    assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("G,M", [(4, 1), (8, 4)])
+@pytest.mark.parametrize("size,scale", [(0.0, SCALE), (0.0, 1e-20), (0.0, 2.0 ** -126), (2.0 ** -120, 2.0 ** -100)])
+def test_rows_without_logits_weigh_all_tokens_alike(G, M, size, scale):
+    """Logits of 0, or below 2^-180: a row's output is the mean of the values it sees (P and its sum are exact, so
+    the sum of the values, cut by 2^-23 of it at most 18 times in each MMA step, is what is off), its lse the
+    logarithm of their number, and its weights 1 over it."""
+    n, H = 200, 2
+    lay, kv, c = cache([n], H, G)
+    q = (rand_bf16((1, M, H * G, 128), 3, 0).double() * size).to(torch.bfloat16)
+    out, lse, acc = run(c, q, scale)
+    V = SC.unpack_tile(kv.numpy())[1]
+    for h in range(H):
+        v = SC.gather(V, None, 0, lay.max_blocks, h, n)
+        w = np.zeros(n)
+        for i in range(M):
+            seen = n - M + i + 1
+            o, mass = v[:seen].mean(0), np.abs(v[:seen]).mean(0)
+            assert (np.abs(f64(out)[0, i, h * G:(h + 1) * G] - o) <= mass * 2.0 ** -16).all()
+            assert np.abs(f64(lse)[0, i, h * G:(h + 1) * G] - np.log(seen)).max() <= 2.0 ** -20
+            w[:seen] += G / seen
+        assert np.abs(SC.gather(f64(acc), None, 0, lay.max_blocks, h, n) / w - 1).max() <= 2.0 ** -18
+    assert int(c.status.item()) == 0
