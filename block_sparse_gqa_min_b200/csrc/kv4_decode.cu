@@ -563,13 +563,14 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_kv4_kernel(A
         for (int x = 0; x < NH; ++x) {
             const int r = 8 * x + warp;
             float f;
-            join(lane < kWarps ? ml[lane % kWarps][r][0] : -INFINITY, lane < kWarps ? ml[lane % kWarps][r][1] : 0.f, f,
-                 row_m[x], row_l[x]);
+            const float l = lane < kWarps ? ml[lane % kWarps][r][1] : 0.f;
+            join(lane < kWarps ? ml[lane % kWarps][r][0] : -INFINITY, l, f, row_m[x], row_l[x]);
+            const uint32_t saw = __ballot_sync(0xffffffffu, l != 0.f);
             acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float fw = __shfl_sync(0xffffffffu, f, w);
-                if (fw != 0.f)  // (a warp without strips left its ring as it was)
+                if (saw >> w & 1)  // (a warp that saw nothing left its ring as it was; a NaN counts whatever its weight)
                     add_weighted(acc[x], fw, *reinterpret_cast<const float4*>(
                         reinterpret_cast<const float*>(ring + w * L::kWarpRing) + r * kRowStride + 4 * lane));
             }

@@ -69,3 +69,27 @@ def test_rows_without_logits_weigh_all_tokens_alike(G, M, size, scale):
             w[:seen] += G / seen
         assert np.abs(SC.gather(f64(acc), None, 0, lay.max_blocks, h, n) / w - 1).max() <= 2.0 ** -18
     assert int(c.status.item()) == 0
+
+
+@pytest.mark.parametrize("token", [1, 40, 150, 260, 3000])
+def test_a_nan_value_is_seen_however_small_its_weight(token):
+    """One token takes all the weight (the others' underflow); a NaN among a seen token's values is in the output
+    all the same, wherever the token's strip was worked on, and nothing else changes."""
+    n, H, G = 4000, 1, 4
+    lay, kv, c = cache([n], H, G)
+    q = torch.zeros((1, 1, H * G, 128), dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    top = 20
+    for j in range(lay.max_blocks):                            # channel 0 of the keys: 6 in one token, -6 in all others
+        kv[j, 0, :, 0:2048:64] = (kv[j, 0, :, 0:2048:64] & 0xF0) | 0xF
+        kv[j, 0, :, 4096:4352:8] = 15 * 8
+    kv[top // 64, 0, top % 64 // 32, top % 32 * 64] &= 0xF7
+    c.kv.copy_(kv)
+    clean = run(c, q, 1e6)[0]
+    V = SC.unpack_tile(kv.numpy())[1]
+    assert np.array_equal(f64(clean)[0, 0, 0], V[0, 0, top])
+    kv[token // 64, 0, token % 64 // 32, 4352 + token % 32 * 8 + 2] = 255
+    c.kv.copy_(kv)
+    got = run(c, q, 1e6)[0]
+    assert torch.isnan(got[..., 32:48]).all()
+    assert torch.equal(got[..., :32], clean[..., :32]) and torch.equal(got[..., 48:], clean[..., 48:])
