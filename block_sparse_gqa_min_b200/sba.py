@@ -532,6 +532,15 @@ def _selection(st, device: int, sel_idx, sel_cnt):
             _tensor(sel_cnt, torch.int32, device, st.B * st.H_kv, "sel_cnt"), shape[2])
 
 
+def _window(st, device: int, k: torch.Tensor, v: torch.Tensor, names):
+    """Addresses of K and V rows [B][n][H_kv][d] and n."""
+    n = k.shape[1] if k.dim() == 4 else -1
+    for t, name in zip((k, v), names):
+        if t.shape != (st.B, n, st.H_kv, st.d):
+            raise ValueError(f"{name} must be bf16 [B][n][H_kv][d] with the same n as {names[0]} (got {tuple(t.shape)})")
+    return (_tensor(k, torch.bfloat16, device, 0, names[0]), _tensor(v, torch.bfloat16, device, 0, names[1])), n
+
+
 def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_params:
     return sba_evict_params(n_keep, n_sink, n_recent)
 
@@ -539,23 +548,17 @@ def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_p
 def sba_append_kv4(c: Cache4, k_new: torch.Tensor, v_new: torch.Tensor, pos_start: torch.Tensor, stream=None):
     """k_new, v_new: bf16 [B][n_new][H_kv][d] to positions pos_start[s] .. of a four-bit cache."""
     ref, st, dev = _opened(c)
-    n_new = k_new.shape[1]
-    rows = st.B * n_new * st.H_kv * st.d
-    _check(load().sba_append_kv4(ref, _tensor(k_new, torch.bfloat16, dev, rows, "k_new"),
-                                 _tensor(v_new, torch.bfloat16, dev, rows, "v_new"),
-                                 _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n_new,
+    (kp, vp), n_new = _window(st, dev, k_new, v_new, ("k_new", "v_new"))
+    _check(load().sba_append_kv4(ref, kp, vp, _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n_new,
                                  _current(dev, stream)), "sba_append_kv4")
 
 
 def sba_read_kv4(c: Cache4, pos_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
     """Positions pos_start[s] .. as bf16 rows k_out, v_out [B][n][H_kv][d]."""
     ref, st, dev = _opened(c)
-    n = k_out.shape[1]
-    rows = st.B * n * st.H_kv * st.d
-    _check(load().sba_read_kv4(ref, _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n,
-                               _tensor(k_out, torch.bfloat16, dev, rows, "k_out"),
-                               _tensor(v_out, torch.bfloat16, dev, rows, "v_out"), _current(dev, stream)),
-           "sba_read_kv4")
+    (kp, vp), n = _window(st, dev, k_out, v_out, ("k_out", "v_out"))
+    _check(load().sba_read_kv4(ref, _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n, kp, vp,
+                               _current(dev, stream)), "sba_read_kv4")
 
 
 def sba_score_select_kv4_workspace_size(c: Cache4, p: sba_select_params) -> int:
