@@ -537,7 +537,8 @@ def _window(st, device: int, k: torch.Tensor, v: torch.Tensor, names):
     n = k.shape[1] if k.dim() == 4 else -1
     for t, name in zip((k, v), names):
         if t.shape != (st.B, n, st.H_kv, st.d):
-            raise ValueError(f"{name} must be bf16 [B][n][H_kv][d] with the same n as {names[0]} (got {tuple(t.shape)})")
+            raise ValueError(f"{name} must be bf16 [B][n][H_kv][d] with the same n as {names[0]} "
+                             f"(got {tuple(t.shape)})")
     return (_tensor(k, torch.bfloat16, device, 0, names[0]), _tensor(v, torch.bfloat16, device, 0, names[1])), n
 
 
@@ -592,8 +593,8 @@ def sba_decode_kv4(c: Cache4, q: torch.Tensor, softmax_scale: float, out: torch.
     if dt is not torch.bfloat16 and dt is not torch.float32:
         raise ValueError("out must be fp32 or bf16")
     rows = st.B * M * st.H_q
-    _check(load().sba_decode_kv4(ref, qp, M, si, sc, n_max, softmax_scale, _tensor(out, dt, dev, rows * st.d, "out"),
-                                 SBA_OUT_BF16 if dt is torch.bfloat16 else SBA_OUT_F32,
+    _check(load().sba_decode_kv4(ref, qp, M, si, sc, n_max, float(softmax_scale),
+                                 _tensor(out, dt, dev, rows * st.d, "out"), SBA_OUT_BF16 if dt is torch.bfloat16 else SBA_OUT_F32,
                                  _tensor(lse_out, torch.float32, dev, rows, "lse_out"),
                                  _tensor(ws, torch.uint8, dev, 0, "ws"), ws.numel(), _current(dev, stream)),
            "sba_decode_kv4")
@@ -616,7 +617,7 @@ def sba_accumulate_weights(c: Cache, q: torch.Tensor, lse: torch.Tensor, softmax
     ref, st, dev = _opened(c)
     qp, M, si, sc, n_max, lp, ai, ao = _weights_args(st, dev, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
     gb = _tensor(gate_bias, torch.float32, dev, st.B * st.H_q * n_max, "gate_bias")
-    _check(load().sba_accumulate_weights(ref, qp, M, si, sc, gb, n_max, softmax_scale, lp, ai, ao,
+    _check(load().sba_accumulate_weights(ref, qp, M, si, sc, gb, n_max, float(softmax_scale), lp, ai, ao,
                                          _current(dev, stream)), "sba_accumulate_weights")
 
 
@@ -626,7 +627,7 @@ def sba_accumulate_weights_kv4(c: Cache4, q: torch.Tensor, lse: torch.Tensor, so
     """sba_accumulate_weights on a four-bit cache."""
     ref, st, dev = _opened(c)
     qp, M, si, sc, n_max, lp, ai, ao = _weights_args(st, dev, q, lse, acc_in, acc_out, sel_idx, sel_cnt)
-    _check(load().sba_accumulate_weights_kv4(ref, qp, M, si, sc, n_max, softmax_scale, lp, ai, ao,
+    _check(load().sba_accumulate_weights_kv4(ref, qp, M, si, sc, n_max, float(softmax_scale), lp, ai, ao,
                                              _current(dev, stream)), "sba_accumulate_weights_kv4")
 
 

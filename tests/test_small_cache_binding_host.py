@@ -55,3 +55,19 @@ def test_rows_of_a_window_have_one_shape(calls, c4):
             with pytest.raises(ValueError, match="must be bf16"):
                 sba.sba_read_kv4(c4, pos, k, v)
     assert len(calls.made) == 2
+
+
+def test_the_scale_may_be_any_number(calls, c4):
+    """As in the library's other calls: a numpy number, a tensor of one element."""
+    import numpy as np
+
+    q, out = (torch.zeros((2, 8, 128), dtype=torch.bfloat16) for _ in range(2))
+    lse, acc, ws = torch.zeros((2, 8)), torch.zeros((8, 2, 64)), torch.zeros(64, dtype=torch.uint8)
+    for scale in (np.float32(0.5), torch.tensor(0.5), 1, 0.5):
+        sba.sba_decode_kv4(c4, q, scale, out, ws)
+        sba.sba_accumulate_weights(c4, q, lse, scale, acc, acc)
+        sba.sba_accumulate_weights_kv4(c4, q, lse, scale, acc, acc)
+    assert len(calls.made) == 12
+    for name, args in calls.made:
+        got = [x for x in args if type(x) is float]
+        assert len(got) == 1 and got[0] in (0.5, 1.0), (name, args)
