@@ -240,6 +240,9 @@ class Cache:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_struct", None)  # a replaced tensor has another address; in-place updates keep it
 
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_struct"}  # (holds addresses: not copied)
+
     def struct(self) -> sba_cache:
         st = self.__dict__.get("_struct")
         if st is None:
@@ -465,6 +468,9 @@ class Cache4:
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         self.__dict__.pop("_struct", None)  # a replaced tensor has another address; in-place updates keep it
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_struct"}  # (holds addresses: not copied)
 
     def struct(self) -> sba_cache4:
         st = self.__dict__.get("_struct")

@@ -71,3 +71,19 @@ def test_the_scale_may_be_any_number(calls, c4):
     for name, args in calls.made:
         got = [x for x in args if type(x) is float]
         assert len(got) == 1 and got[0] in (0.5, 1.0), (name, args)
+
+
+def test_caches_can_be_copied():
+    """A cache that has been used (and so holds its C struct) is copied like any dataclass of tensors."""
+    import copy
+    import pickle
+
+    lens = torch.zeros(1, dtype=torch.int32)
+    k = torch.zeros((4, 2, 64, 128), dtype=torch.bfloat16)
+    for c, st in ((sba.Cache4(kv=torch.zeros((4, 2, 2, 4608), dtype=torch.uint8), seq_lens=lens, H_q=4, max_blocks=4,
+                              max_len=256), sba.sba_cache4()),
+                  (sba.Cache(k=k, v=k, seq_lens=lens, H_q=4, max_blocks=4, max_len=256), sba.sba_cache())):
+        c.__dict__["_struct"] = st
+        for other in (copy.copy(c), copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+            assert other.max_len == 256 and torch.equal(other.seq_lens, lens) and "_struct" not in other.__dict__
+        assert copy.copy(c).seq_lens is lens and c.__dict__["_struct"] is st
