@@ -203,7 +203,8 @@ def _check(rc: int, where: str):
 
 @dataclass
 class Cache:
-    """Device tensors of one layer's KV cache and its descriptors (sba_cache)."""
+    """Device tensors of one layer's KV cache and its descriptors (sba_cache).  Their addresses are kept from
+    call to call: to use other memory, set the field to another tensor (a tensor's own storage stays)."""
 
     k: torch.Tensor                        # bf16 [num_pages][H_kv][b][d]
     v: torch.Tensor
@@ -434,7 +435,8 @@ STRIP_BYTES = 4608
 
 @dataclass
 class Cache4:
-    """Device tensors of one layer's four-bit KV cache and its Quest descriptors (sba_cache4)."""
+    """Device tensors of one layer's four-bit KV cache and its Quest descriptors (sba_cache4).  Their addresses
+    are kept from call to call, as Cache's are."""
 
     kv: torch.Tensor                       # uint8 [num_pages][H_kv][b/32][4608]
     seq_lens: torch.Tensor                 # int32 [B]
@@ -600,7 +602,8 @@ def sba_decode_kv4(c: Cache4, q: torch.Tensor, softmax_scale: float, out: torch.
         raise ValueError("out must be fp32 or bf16")
     rows = st.B * M * st.H_q
     _check(load().sba_decode_kv4(ref, qp, M, si, sc, n_max, float(softmax_scale),
-                                 _tensor(out, dt, dev, rows * st.d, "out"), SBA_OUT_BF16 if dt is torch.bfloat16 else SBA_OUT_F32,
+                                 _tensor(out, dt, dev, rows * st.d, "out"),
+                                 SBA_OUT_BF16 if dt is torch.bfloat16 else SBA_OUT_F32,
                                  _tensor(lse_out, torch.float32, dev, rows, "lse_out"),
                                  _tensor(ws, torch.uint8, dev, 0, "ws"), ws.numel(), _current(dev, stream)),
            "sba_decode_kv4")
