@@ -3,6 +3,8 @@
 // or synchronises.
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "kv4.cuh"
 #include "launch.cuh"
@@ -310,7 +312,12 @@ int sba_decode_step(const sba_cache* c, const void* q, const void* k_new, const 
 namespace {
 
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// 32-bit words (NULL, an argument that is not there, passes).
+bool aligned4(std::initializer_list<const void*> words) {
+    for (const void* p : words)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
+    return true;
+}
 
 // A four-bit cache seen as a bf16 one: the same checks, and the view that scoring (which reads the
 // descriptors only) takes.
@@ -339,7 +346,7 @@ int check_cache4(const sba_cache4* c) {
     const int rc = check_cache(&v);
     if (rc != SBA_OK) return rc;
     if (c->B > 65535 || c->H_kv > 65535) return SBA_ERR_UNSUPPORTED;
-    return SBA_OK;
+    return aligned4({c->block_table, c->seq_lens, c->status}) ? SBA_OK : SBA_ERR_INVALID_ARG;
 }
 
 // Arguments of the calls that attend with M query tokens over a selection or (sel_idx NULL) all blocks.
@@ -347,14 +354,14 @@ int check_attend(int B, int H_q, int H_kv, const void* q, int32_t M, const int32
                  int32_t n_max, float softmax_scale) {
     if (!q || !aligned16(q) || M < 1 || M > kMaxQueryTokens || !good_scale(softmax_scale)) return SBA_ERR_INVALID_ARG;
     if (sel_idx ? (!sel_cnt || n_max < 1) : (sel_cnt != nullptr || n_max != 0)) return SBA_ERR_INVALID_ARG;
+    if (!aligned4({sel_idx, sel_cnt})) return SBA_ERR_INVALID_ARG;
     const int64_t groups = (int64_t)H_kv * (((int64_t)M * (H_q / H_kv) + 7) / 8);
     if (groups > 65535 || groups * B >= (int64_t)1 << 31) return SBA_ERR_UNSUPPORTED;
     return SBA_OK;
 }
 
 int check_weights(const float* lse, const float* acc_in, const float* acc_out) {
-    if (!lse || !acc_in || !acc_out || !aligned4(lse) || !aligned4(acc_in) || !aligned4(acc_out))
-        return SBA_ERR_INVALID_ARG;
+    if (!lse || !acc_in || !acc_out || !aligned4({lse, acc_in, acc_out})) return SBA_ERR_INVALID_ARG;
     return SBA_OK;
 }
 
@@ -367,7 +374,9 @@ bool overlap(const float* x, size_t nx, const float* y, size_t ny) {
 // Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before).
 int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* p, const sba_cache& dst,
                 const float* acc_dst, const int32_t* new_lens, const int32_t* kept) {
-    if (!acc || !aligned16(acc) || !p || !new_lens || !kept) return SBA_ERR_INVALID_ARG;
+    if (!acc || !aligned16(acc) || !p || !new_lens || !kept || !aligned4({acc_dst, new_lens, kept}))
+        return SBA_ERR_INVALID_ARG;
+    if (!aligned4({src.block_table, src.seq_lens, src.status, dst.block_table, dst.status})) return SBA_ERR_INVALID_ARG;
     if (p->n_keep < 1 || p->n_sink < 0 || p->n_recent < 0 || (int64_t)p->n_sink + p->n_recent > p->n_keep)
         return SBA_ERR_INVALID_ARG;
     if (dst.B != src.B || dst.H_kv != src.H_kv || dst.b != src.b) return SBA_ERR_INVALID_ARG;
@@ -394,7 +403,7 @@ int sba_append_kv4(const sba_cache4* c, const void* k_new, const void* v_new, co
     const int rc = check_cache4(c);
     if (rc != SBA_OK) return rc;
     if (!k_new || !v_new || !pos_start || n_new < 0) return SBA_ERR_INVALID_ARG;
-    if (!aligned32(k_new) || !aligned32(v_new)) return SBA_ERR_INVALID_ARG;
+    if (!aligned32(k_new) || !aligned32(v_new) || !aligned4({pos_start})) return SBA_ERR_INVALID_ARG;
     if (n_new == 0) return SBA_OK;
     return after_launch(launch_append_kv4(*c, k_new, v_new, pos_start, n_new, static_cast<cudaStream_t>(stream)));
 }
@@ -403,7 +412,7 @@ int sba_read_kv4(const sba_cache4* c, const int32_t* pos_start, int32_t n, void*
     const int rc = check_cache4(c);
     if (rc != SBA_OK) return rc;
     if (!k_out || !v_out || !pos_start || n < 0) return SBA_ERR_INVALID_ARG;
-    if (!aligned32(k_out) || !aligned32(v_out)) return SBA_ERR_INVALID_ARG;
+    if (!aligned32(k_out) || !aligned32(v_out) || !aligned4({pos_start})) return SBA_ERR_INVALID_ARG;
     if (n == 0) return SBA_OK;
     return after_launch(launch_read_kv4(*c, pos_start, n, k_out, v_out, static_cast<cudaStream_t>(stream)));
 }
@@ -435,6 +444,7 @@ int sba_decode_kv4(const sba_cache4* c, const void* q, int32_t M, const int32_t*
     rc = check_attend(c->B, c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
     if (rc != SBA_OK) return rc;
     if (!out || !aligned16(out) || (out_dtype != SBA_OUT_F32 && out_dtype != SBA_OUT_BF16)) return SBA_ERR_INVALID_ARG;
+    if (!aligned4({lse_out})) return SBA_ERR_INVALID_ARG;
     if (!ws || !aligned16(ws) || ws_bytes < decode_kv4_workspace_bytes(*c, M, n_max)) return SBA_ERR_WORKSPACE;
     return after_launch(launch_decode_kv4(*c, q, M, sel_idx, sel_cnt, n_max, softmax_scale, out, out_dtype, lse_out, ws,
                                           static_cast<cudaStream_t>(stream)));
@@ -447,7 +457,8 @@ int sba_accumulate_weights(const sba_cache* c, const void* q, int32_t M, const i
     if (rc != SBA_OK) return rc;
     rc = check_attend(c->B, c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
     if (rc != SBA_OK) return rc;
-    if (gate_bias && (!sel_idx || M != 1)) return SBA_ERR_INVALID_ARG;
+    if (gate_bias && (!sel_idx || M != 1 || !aligned4({gate_bias}))) return SBA_ERR_INVALID_ARG;
+    if (!aligned4({c->block_table, c->seq_lens, c->status})) return SBA_ERR_INVALID_ARG;
     rc = check_weights(lse, acc_in, acc_out);
     if (rc != SBA_OK) return rc;
     if (c->B > 65535 || c->H_kv > 65535) return SBA_ERR_UNSUPPORTED;
