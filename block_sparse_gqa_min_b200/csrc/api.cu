@@ -360,15 +360,17 @@ int check_attend(int B, int H_q, int H_kv, const void* q, int32_t M, const int32
     return SBA_OK;
 }
 
-int check_weights(const float* lse, const float* acc_in, const float* acc_out) {
-    if (!lse || !acc_in || !acc_out || !aligned4({lse, acc_in, acc_out})) return SBA_ERR_INVALID_ARG;
-    return SBA_OK;
-}
-
-size_t cells(const sba_cache& c) { return (size_t)c.num_pages * c.H_kv * c.b; }
+size_t cells(int num_pages, int H_kv, int b) { return (size_t)num_pages * H_kv * b; }
 bool overlap(const float* x, size_t nx, const float* y, size_t ny) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
     return x && y && a < b + ny * 4 && b < a + nx * 4;
+}
+
+// A token's sum is read and written by one thread: in place is fine, one array shifted over the other is not.
+int check_weights(const float* lse, const float* acc_in, const float* acc_out, size_t n) {
+    if (!lse || !acc_in || !acc_out || !aligned4({lse, acc_in, acc_out})) return SBA_ERR_INVALID_ARG;
+    if (acc_in != acc_out && overlap(acc_in, n, acc_out, n)) return SBA_ERR_INVALID_ARG;
+    return SBA_OK;
 }
 
 // Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before).
@@ -391,7 +393,10 @@ int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* 
     const bool one_pool = dst.k == src.k && dst.v == src.v;
     if (!src.block_table && !dst.block_table && (dst.k == src.k || dst.v == src.v)) return SBA_ERR_INVALID_ARG;
     if (dst.desc && dst.desc == src.desc && !dst.block_table && !(one_pool && src.block_table)) return SBA_ERR_INVALID_ARG;
-    if (acc_dst == acc ? !one_pool : overlap(acc, cells(src), acc_dst, cells(dst))) return SBA_ERR_INVALID_ARG;
+    if (acc_dst == acc ? !one_pool
+                       : overlap(acc, cells(src.num_pages, src.H_kv, src.b), acc_dst,
+                                 cells(dst.num_pages, dst.H_kv, dst.b)))
+        return SBA_ERR_INVALID_ARG;
     if (src.B > 65535 || src.H_kv > 65535) return SBA_ERR_UNSUPPORTED;
     return SBA_OK;
 }
@@ -459,7 +464,7 @@ int sba_accumulate_weights(const sba_cache* c, const void* q, int32_t M, const i
     if (rc != SBA_OK) return rc;
     if (gate_bias && (!sel_idx || M != 1 || !aligned4({gate_bias}))) return SBA_ERR_INVALID_ARG;
     if (!aligned4({c->block_table, c->seq_lens, c->status})) return SBA_ERR_INVALID_ARG;
-    rc = check_weights(lse, acc_in, acc_out);
+    rc = check_weights(lse, acc_in, acc_out, cells(c->num_pages, c->H_kv, c->b));
     if (rc != SBA_OK) return rc;
     if (c->B > 65535 || c->H_kv > 65535) return SBA_ERR_UNSUPPORTED;
     return after_launch(launch_accumulate_weights(*c, q, M, sel_idx, sel_cnt, gate_bias, n_max, softmax_scale, lse,
@@ -473,7 +478,7 @@ int sba_accumulate_weights_kv4(const sba_cache4* c, const void* q, int32_t M, co
     if (rc != SBA_OK) return rc;
     rc = check_attend(c->B, c->H_q, c->H_kv, q, M, sel_idx, sel_cnt, n_max, softmax_scale);
     if (rc != SBA_OK) return rc;
-    rc = check_weights(lse, acc_in, acc_out);
+    rc = check_weights(lse, acc_in, acc_out, cells(c->num_pages, c->H_kv, c->b));
     if (rc != SBA_OK) return rc;
     return after_launch(launch_accumulate_weights_kv4(*c, q, M, sel_idx, sel_cnt, n_max, softmax_scale, lse, acc_in,
                                                       acc_out, static_cast<cudaStream_t>(stream)));

@@ -497,7 +497,7 @@ int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t 
  *               gates of an attention that has them in its logits (inner: the rows' weights sum to 1) or
  *               on its values (outer: lse is that of the ungated logits, so the sum is what each value
  *               entered the output with, gate included); NULL where the gate only selects.
- * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); may be the same.
+ * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); the same, or apart.
  * A token that has just been appended needs acc_in 0 in its cells: no call clears them.
  * A selection lists every block once, ascending; an entry that is not larger than the one before it is
  * skipped and reports SBA_DEV_BAD_SELECTION (what a list that still names a block twice adds to that

@@ -28,3 +28,14 @@ def test_words_have_to_be_aligned():
         assert lib.sba_append_kv4(c4(**bad), 0x8000, 0x9000, 0x7000, 1, None) == ARG
         assert lib.sba_evict(c16(**bad), 0x5000, p, c16(k=0x100000, v=0x200000, desc=None), None, 0x7000, 0x8000, None) == ARG
         assert lib.sba_accumulate_weights(c16(**bad), 0x5000, 1, None, None, None, 0, 0.1, 0xa000, 0xb000, 0xb000, None) == ARG
+
+
+def test_sums_in_place_or_apart():
+    lib, size = sba.load(), 64 * 2 * 64 * 4
+    a = 0x100000
+    for o in (a + 4, a - 4, a + size - 4, a - size + 4):
+        assert lib.sba_accumulate_weights(c16(), 0x5000, 1, None, None, None, 0, 0.1, 0xa000, a, o, None) == ARG
+        assert lib.sba_accumulate_weights_kv4(c4(), 0x5000, 1, None, None, 0, 0.1, 0xa000, a, o, None) == ARG
+    for o in (a, a + size, a - size):       # past the checks: no GPU to launch on
+        assert lib.sba_accumulate_weights(c16(), 0x5000, 1, None, None, None, 0, 0.1, 0xa000, a, o, None) == sba.SBA_ERR_CUDA
+        assert lib.sba_accumulate_weights_kv4(c4(), 0x5000, 1, None, None, 0, 0.1, 0xa000, a, o, None) == sba.SBA_ERR_CUDA
