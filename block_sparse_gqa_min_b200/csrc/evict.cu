@@ -61,8 +61,7 @@ __device__ __forceinline__ int clamped_len(const int32_t* seq_lens, int s, int m
 
 // Larger for a larger weight, the same for both zeros; 1 for a NaN.
 __device__ __forceinline__ uint32_t key_of(float w) {
-    const uint32_t u = __float_as_uint(w + 0.f);
-    return w != w ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return w != w ? 1u : orderable_key(w);
 }
 
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(SelectArgs a, int cap) {
@@ -460,7 +459,6 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(MoveArgs a) {
     __shared__ int64_t src[kBlk];
     __shared__ uint32_t red[2][kMoveThreads / 32][64];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = tid & 15, r0 = tid >> 4;
-    pdl_wait();
     pdl_trigger();
     int64_t page = -1;
     if (source_rows<kBlk>(a, src, page) == 0) return;
@@ -523,7 +521,6 @@ __global__ void __launch_bounds__(kMove4Threads, kBlk == 64 ? 12 : 8) evict_move
     __shared__ int64_t src[kBlk];
     __shared__ __half2 red[2][64][kRowsAt + 1];
     const int tid = threadIdx.x, lane = tid & 31, g = tid & 7, r = tid >> 3;
-    pdl_wait();
     pdl_trigger();
     int64_t page = -1;
     if (source_rows<kBlk>(a, src, page) == 0) return;
@@ -663,7 +660,7 @@ int launch_select(const Cache& src, const float* acc, const sba_evict_params& p,
 }
 
 // In plain stream order: launched early, its CTAs waited on the SMs that the selection left idle, and
-// evict_512k took 71 us instead of 66.
+// evict_512k took 71 us instead of 66.  (The kernel after it may start early: that is its own launch's attribute.)
 int launch_move(void (*kernel)(MoveArgs), dim3 grid, int threads, const MoveArgs& m, cudaStream_t stream) {
     kernel<<<grid, threads, 0, stream>>>(m);
     return SBA_OK;  // the caller looks at cudaGetLastError
