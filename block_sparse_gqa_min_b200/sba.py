@@ -541,13 +541,14 @@ def _selection(st, device: int, sel_idx, sel_cnt):
 
 
 def _window(st, device: int, k: torch.Tensor, v: torch.Tensor, names):
-    """Addresses of K and V rows [B][n][H_kv][d] and n."""
-    n = k.shape[1] if k.dim() == 4 else -1
-    for t, name in zip((k, v), names):
-        if t.shape != (st.B, n, st.H_kv, st.d):
-            raise ValueError(f"{name} must be bf16 [B][n][H_kv][d] with the same n as {names[0]} "
-                             f"(got {tuple(t.shape)})")
-    return (_tensor(k, torch.bfloat16, device, 0, names[0]), _tensor(v, torch.bfloat16, device, 0, names[1])), n
+    """Addresses of K and V rows [B][n][H_kv][d], and n."""
+    at = k.shape
+    n = at[1] if len(at) == 4 else -1
+    want = (st.B, n, st.H_kv, 128)
+    if at != want or v.shape != want:
+        raise ValueError(f"{names[0]} and {names[1]} must be bf16 [B][n][H_kv][128] with the same n "
+                         f"(got {tuple(at)} and {tuple(v.shape)})")
+    return _tensor(k, torch.bfloat16, device, 0, names[0]), _tensor(v, torch.bfloat16, device, 0, names[1]), n
 
 
 def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_params:
@@ -557,7 +558,7 @@ def evict_params(n_keep: int, n_sink: int = 0, n_recent: int = 0) -> sba_evict_p
 def sba_append_kv4(c: Cache4, k_new: torch.Tensor, v_new: torch.Tensor, pos_start: torch.Tensor, stream=None):
     """k_new, v_new: bf16 [B][n_new][H_kv][d] to positions pos_start[s] .. of a four-bit cache."""
     ref, st, dev = _opened(c)
-    (kp, vp), n_new = _window(st, dev, k_new, v_new, ("k_new", "v_new"))
+    kp, vp, n_new = _window(st, dev, k_new, v_new, ("k_new", "v_new"))
     _check(load().sba_append_kv4(ref, kp, vp, _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n_new,
                                  _current(dev, stream)), "sba_append_kv4")
 
@@ -565,7 +566,7 @@ def sba_append_kv4(c: Cache4, k_new: torch.Tensor, v_new: torch.Tensor, pos_star
 def sba_read_kv4(c: Cache4, pos_start: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor, stream=None):
     """Positions pos_start[s] .. as bf16 rows k_out, v_out [B][n][H_kv][d]."""
     ref, st, dev = _opened(c)
-    (kp, vp), n = _window(st, dev, k_out, v_out, ("k_out", "v_out"))
+    kp, vp, n = _window(st, dev, k_out, v_out, ("k_out", "v_out"))
     _check(load().sba_read_kv4(ref, _tensor(pos_start, torch.int32, dev, st.B, "pos_start"), n, kp, vp,
                                _current(dev, stream)), "sba_read_kv4")
 
