@@ -145,6 +145,7 @@ constexpr int kStripVS = 4352;   // value scales
 constexpr int kStripBytes = 4608;
 constexpr uint32_t kScaleMaxByte = 226;  // 10240: 6 * 10240 still fits f16
 constexpr uint32_t kScaleNaN = 0xff;     // a group that held a NaN or an infinity reads back as NaN
+constexpr uint32_t kScaleInf = 0xf8;     // from here on bytes are no numbers (infinity, NaN); only kScaleNaN is given out
 
 // Eight codes -> eight f16 (pairs of neighbouring channels, the even one in the low half).
 __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {

@@ -131,11 +131,11 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
         __syncwarp();
     }
     if (partial && first_hidden < tok0 + valid) {
-        // some rows do not see the last tokens: a NaN among those tokens' values must reach only the
+        // some rows do not see the last tokens: a NaN (or infinity) among those tokens' values must reach only the
         // rows that do (0 * NaN is NaN in the product below), so it is put there by hand
         const int t0 = max(0, first_hidden - tok0);
         for (int t = t0; t < valid; ++t)
-            if (strip[kStripVS + t * 8 + tr] == kScaleNaN) {
+            if (strip[kStripVS + t * 8 + tr] >= kScaleInf) {
 #pragma unroll
                 for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
@@ -146,7 +146,7 @@ __device__ __forceinline__ void attend_strip(State<NH>& st, const uint32_t (&qb)
             }
         __syncwarp();
         for (int e = t0 * 8 + lane; e < valid * 8; e += 32)
-            if (strip[kStripVS + e] == kScaleNaN) strip[kStripVS + e] = 0;
+            if (strip[kStripVS + e] >= kScaleInf) strip[kStripVS + e] = 0;
         fence_proxy_async_smem();
         __syncwarp();
     }

@@ -171,7 +171,9 @@ typedef struct sba_select_params {
  *               c/2: sign, then one of 0, .5, 1, 1.5, 2, 3, 4, 6 (e2m1).  Scale byte g belongs to
  *               channels 16g .. 16g+15: five exponent bits (bias 15) and three mantissa bits, the top
  *               byte of a positive f16 below its sign (byte << 7 are its bits).  A value is
- *               code * scale; it is exact in f16 and in bf16.
+ *               code * scale; it is exact in f16 and in bf16.  sba_append_kv4 gives out the bytes 0 .. 226
+ *               and 255 (NaN); what the others from 248 on do to a row that sees their token is not
+ *               defined further than not finite.
  * desc          Quest descriptors of the keys AS HELD, bf16 [num_pages][H_kv][2][d], or NULL.
  *
  * Only the Quest scorer has a four-bit form (a gate key is formed from bf16 keys). */
@@ -499,6 +501,8 @@ int sba_decode_kv4(const sba_cache4 *c, const void *q, int32_t M, const int32_t 
  *               entered the output with, gate included); NULL where the gate only selects.
  * acc_in/out    device fp32 [num_pages][H_kv][b] (indexed like the cache's rows); the same, or apart.
  * A token that has just been appended needs acc_in 0 in its cells: no call clears them.
+ * A page belongs to one sequence of a call (the sums of a page that two sequences share would be written by
+ * both at once).
  * A selection lists every block once, ascending; an entry that is not larger than the one before it is
  * skipped and reports SBA_DEV_BAD_SELECTION (what a list that still names a block twice adds to that
  * block is not defined).  No atomics: the same inputs give the same bits. */

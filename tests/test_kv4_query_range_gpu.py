@@ -93,3 +93,19 @@ def test_a_nan_value_is_seen_however_small_its_weight(token):
     got = run(c, q, 1e6)[0]
     assert torch.isnan(got[..., 32:48]).all()
     assert torch.equal(got[..., :32], clean[..., :32]) and torch.equal(got[..., 48:], clean[..., 48:])
+
+
+@pytest.mark.parametrize("byte", [248, 249, 254, 255])
+def test_scales_that_are_no_numbers_stay_with_the_rows_that_see_them(byte):
+    """Any byte whose exponent bits are all ones, in a token that the first of several query tokens do not see:
+    their rows do not change by a bit, the others' 16 channels are NaN."""
+    n, H, G, M, t = 200, 1, 2, 4, 198                          # tokens 196 .. 199 ask; 198 is hidden from two
+    lay, kv, c = cache([n], H, G)
+    q = rand_bf16((1, M, H * G, 128), 3, 0)
+    clean, clean_lse, _ = run(c, q, SCALE)
+    kv[t // 64, 0, t % 64 // 32, 4352 + t % 32 * 8 + 5] = byte
+    c.kv.copy_(kv)
+    out, lse, _ = run(c, q, SCALE)
+    assert torch.equal(out[:, :2], clean[:, :2]) and torch.equal(lse, clean_lse)
+    assert torch.isnan(out[:, 2:, :, 80:96]).all()
+    assert torch.equal(out[:, 2:, :, :80], clean[:, 2:, :, :80]) and torch.equal(out[:, 2:, :, 96:], clean[:, 2:, :, 96:])
