@@ -474,8 +474,8 @@ int sba_score_select_kv4(const sba_cache4 *c, const void *q, int32_t M, const sb
  *                   [B][H_kv][n_max], [B][H_kv]); or both NULL with n_max = 0: every block.  A block
  *                   listed twice is attended to twice.
  * out       device [B][M][H_q][d] in out_dtype (SBA_OUT_F32 or SBA_OUT_BF16), 16-byte aligned;
- *           0 for a row that sees no token.  Both types come from the same fp32 result (weights and sums are
- *           held in more than 20 bits throughout); bf16 rounds it once.
+ *           0 for a row that sees no token.  Weights enter the product in more than 20 bits, sums are
+ *           fp32: an fp32 output is as exact as a plain fp32 form's, a bf16 one is rounded once.
  * lse_out   device fp32 [B][M][H_q] or NULL: log sum exp of the row's logits, -inf if it sees none.
  * ws        device workspace of at least sba_decode_kv4_workspace_size() bytes, 16-byte aligned,
  *           ZERO-FILLED before its first use; every completed call leaves its counters at zero again, so
