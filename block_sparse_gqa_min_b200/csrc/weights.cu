@@ -120,7 +120,7 @@ struct Keys<true> {  // channels 32i .. 32i + 31: one 16-byte read a row
 template <bool kFour, bool kShared>
 __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a) {
     __shared__ uint2 qf[kRowTiles][8][32];
-    __shared__ float row_sc[kRowTiles * 8], row_lse[kRowTiles * 8];
+    __shared__ float row_sc[kRowTiles * 8], row_lse[kRowTiles * 8];  // lse in log2 units, or as it is under a bias
     __shared__ int row_lim[kRowTiles * 8];
     __shared__ int tile_plain[kRowTiles];  // every row of the tile is real and has a finite lse
 
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
             const bool counts = lse > -INFINITY || lse != lse;  // a row that attended to nothing adds nothing
             if (qi == 0) {
                 row_sc[t * 8 + tr] = a.scale_log2 * up;
-                row_lse[t * 8 + tr] = counts ? lse * kLog2e : 0.f;
+                row_lse[t * 8 + tr] = !counts ? 0.f : a.gate_bias ? lse : lse * kLog2e;
                 row_lim[t * 8 + tr] = counts ? len - a.M + r / G + 1 : 0;
             }
             const int all = __all_sync(0xffffffffu, counts);
@@ -263,8 +263,9 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
                 float2 off = *reinterpret_cast<const float2*>(&row_lse[r]);
                 if (a.gate_bias) {
                     const int64_t at = ((int64_t)s * a.H_q + h * G + r) * a.n_max + cur_pos;
-                    if (r < a.rows) off.x -= __ldca(a.gate_bias + at) * kLog2e;
-                    if (r + 1 < a.rows) off.y -= __ldca(a.gate_bias + at + a.n_max) * kLog2e;
+                    // (lse - bias first: where both are the type's lowest value, either in log2 units is infinite)
+                    if (r < a.rows) off.x = (off.x - __ldca(a.gate_bias + at)) * kLog2e;
+                    if (r + 1 < a.rows) off.y = (off.y - __ldca(a.gate_bias + at + a.n_max)) * kLog2e;
                 }
                 float p0 = ex2(fmaf(e[0] + o[0], sc.x, -off.x)), p1 = ex2(fmaf(e[1] + o[1], sc.y, -off.y));
                 float p2 = ex2(fmaf(e[2] + o[2], sc.x, -off.x)), p3 = ex2(fmaf(e[3] + o[3], sc.y, -off.y));
