@@ -10,7 +10,7 @@
 // read straight from global memory into operand registers, with the next tile's keys in flight; the
 // query rows are the columns, 8 at a time, kept in shared memory as operand fragments.  The channels
 // of an MMA step are permuted alike in both so that every lane's key reads are 16 bytes.
-// With few rows the bytes of K bound it: bf16, 8 sequences of 32-64K, 8 KV heads, 4 rows: 135 us, 94% of the
+// With few rows the bytes of K bound it: bf16, 8 sequences of 48K, 8 KV heads, 4 rows: 133 us, 93% of the
 // copy bandwidth; a gated step's 32 blocks of 64 tokens: 4.5 us.  Many rows, and long four-bit launches, go to
 // the second kernel below.
 #include <math.h>
@@ -301,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
 // memory, one thread issues the eight steps of 16 channels against the rows in shared memory, and every
 // thread reads back the 64 logits of ONE token, so the sum over the rows is in its own registers (no
 // shuffle, no shared memory).  What bounds it is the 16 exponentials a cycle of an SM: 64 rows over 393K tokens
-// and 8 KV heads would take 45 us at that rate and take 103 (four bits; 183 in bf16, where the keys alone
-// take 127): the unit is 47% busy, since a tile's steps (codes to f16 0.4 us, products 0.3, exponentials 0.9)
+// and 8 KV heads would take 45 us at that rate and take 104 (four bits; 179 in bf16, where the keys alone
+// take 123; 69 in four bits at 4 rows, where the bytes would take 38): the unit is 47% busy, since a tile's steps (codes to f16 0.4 us, products 0.3, exponentials 0.9)
 // follow one another and tensor memory has room for four tiles an SM.
 // Two CTAs of two warpgroups share an SM; every warpgroup works on tiles of its own, so one's conversion
 // and its wait for the tensor core overlap the others' exponentials.
