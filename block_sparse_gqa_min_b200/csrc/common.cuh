@@ -154,14 +154,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int32_
     return true;
 }
 
-// The same wait by a whole warp, with one verdict: every lane has a clock of its own, and a warp that goes on
-// with full-mask operations must not part where the limit runs out for some lanes just before the phase
-// completes for the others.  False for all if any lane gave up.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int32_t* status,
-                                               uint64_t limit_ns = kWaitTimeoutNs) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, limit_ns));
-}
-
 // The same wait, each try suspending the thread until the phase completes or about
 // `hint_ns` pass: a waiting warp then takes no issue slots from the working ones.
 __device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {

@@ -39,6 +39,15 @@ int launch_evict(const sba_cache& src, const float* acc, const sba_evict_params&
                  float* acc_dst, int32_t* new_lens, int32_t* kept, cudaStream_t stream);
 int launch_evict_kv4(const sba_cache4& src, const float* acc, const sba_evict_params& p, const sba_cache4& dst,
                      float* acc_dst, int32_t* new_lens, int32_t* kept, cudaStream_t stream);
+int launch_wait_vote_selftest(int32_t* status, int32_t* verdicts, uint64_t limit_ns, cudaStream_t stream);
+
+// mbar_wait by a whole warp, with one verdict: every lane has a clock of its own, and a warp that goes on
+// with full-mask operations must not part where the limit runs out for some lanes just before the phase
+// completes for the others.  False for all if any lane gave up.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, int32_t* status,
+                                               uint64_t limit_ns = kWaitTimeoutNs) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, limit_ns));
+}
 
 // 16 bytes that are read once: not kept in L1, and (volatile) never moved above griddepcontrol.wait.
 __device__ __forceinline__ uint4 ld_once_v4(const void* p) {

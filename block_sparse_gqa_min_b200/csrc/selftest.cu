@@ -9,6 +9,7 @@
 // The second test is of mbar_wait_warp: the lanes of a warp wait with different limits, the phase completes
 // in between, and all have to come back with the one verdict that the wait ran out.
 #include "common.cuh"
+#include "kv4.cuh"
 #include "launch.cuh"
 
 namespace sba {
