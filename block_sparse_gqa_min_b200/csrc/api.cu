@@ -373,9 +373,10 @@ int check_weights(const float* lse, const float* acc_in, const float* acc_out, s
     return SBA_OK;
 }
 
-// Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before).
-int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* p, const sba_cache& dst,
-                const float* acc_dst, const int32_t* new_lens, const int32_t* kept) {
+// Arguments of an eviction; src and dst seen as bf16 caches (checked each by itself before), page_bytes those of
+// one of k's pages.
+int check_evict(const sba_cache& src, int64_t page_bytes, const float* acc, const sba_evict_params* p,
+                const sba_cache& dst, const float* acc_dst, const int32_t* new_lens, const int32_t* kept) {
     if (!acc || !aligned16(acc) || !p || !new_lens || !kept || !aligned4({acc_dst, new_lens, kept}))
         return SBA_ERR_INVALID_ARG;
     if (!aligned4({src.block_table, src.seq_lens, src.status, dst.block_table, dst.status})) return SBA_ERR_INVALID_ARG;
@@ -388,15 +389,18 @@ int check_evict(const sba_cache& src, const float* acc, const sba_evict_params* 
     const intptr_t size = (intptr_t)src.B * 4;
     if (apart > -size && apart < size) return SBA_ERR_INVALID_ARG;
     // One pool: the caches' pages are apart only where a block table says so, for without one either begins at
-    // page 0.  Its weights are one array too; weights of different pools, or that overlap in any other way, are
-    // read where others are written.
+    // page 0.
     const bool one_pool = dst.k == src.k && dst.v == src.v;
     if (!src.block_table && !dst.block_table && (dst.k == src.k || dst.v == src.v)) return SBA_ERR_INVALID_ARG;
     if (dst.desc && dst.desc == src.desc && !dst.block_table && !(one_pool && src.block_table)) return SBA_ERR_INVALID_ARG;
-    if (acc_dst == acc ? !one_pool
-                       : overlap(acc, cells(src.num_pages, src.H_kv, src.b), acc_dst,
-                                 cells(dst.num_pages, dst.H_kv, dst.b)))
-        return SBA_ERR_INVALID_ARG;
+    // Its weights are one array too: dst's begin at the page at which dst's rows do.  Weights that overlap in any
+    // other way are read where others are written.
+    if (overlap(acc, cells(src.num_pages, src.H_kv, src.b), acc_dst, cells(dst.num_pages, dst.H_kv, dst.b))) {
+        const intptr_t at = static_cast<const char*>(dst.k) - static_cast<const char*>(src.k);
+        const intptr_t at_v = static_cast<const char*>(dst.v) - static_cast<const char*>(src.v);
+        const intptr_t page = page_bytes, page_acc = (intptr_t)src.H_kv * src.b * 4;
+        if (at != at_v || at % page != 0 || (intptr_t)(acc_dst - acc) * 4 != at / page * page_acc) return SBA_ERR_INVALID_ARG;
+    }
     if (src.B > 65535 || src.H_kv > 65535) return SBA_ERR_UNSUPPORTED;
     return SBA_OK;
 }
@@ -488,7 +492,8 @@ int sba_evict(const sba_cache* src, const float* acc, const sba_evict_params* p,
               int32_t* new_lens, int32_t* kept, void* stream) {
     int rc = check_cache(src);
     if (rc == SBA_OK) rc = check_cache(dst);
-    if (rc == SBA_OK) rc = check_evict(*src, acc, p, *dst, acc_dst, new_lens, kept);
+    if (rc == SBA_OK)
+        rc = check_evict(*src, (int64_t)src->H_kv * src->b * kHeadDim * 2, acc, p, *dst, acc_dst, new_lens, kept);
     if (rc != SBA_OK) return rc;
     return after_launch(launch_evict(*src, acc, *p, *dst, acc_dst, new_lens, kept, static_cast<cudaStream_t>(stream)));
 }
@@ -497,7 +502,9 @@ int sba_evict_kv4(const sba_cache4* src, const float* acc, const sba_evict_param
                   float* acc_dst, int32_t* new_lens, int32_t* kept, void* stream) {
     int rc = check_cache4(src);
     if (rc == SBA_OK) rc = check_cache4(dst);
-    if (rc == SBA_OK) rc = check_evict(view_of(*src), acc, p, view_of(*dst), acc_dst, new_lens, kept);
+    if (rc == SBA_OK)
+        rc = check_evict(view_of(*src), (int64_t)src->H_kv * (src->b / kStripTokens) * kStripBytes, acc, p, view_of(*dst),
+                         acc_dst, new_lens, kept);
     if (rc != SBA_OK) return rc;
     return after_launch(
         launch_evict_kv4(*src, acc, *p, *dst, acc_dst, new_lens, kept, static_cast<cudaStream_t>(stream)));

@@ -26,12 +26,12 @@
 // ring of its own, so no warp waits for another until the merge.
 //
 // Measured on B200: all tokens of 8 sequences of 32-64K, 32/8 heads, bf16 out: 113 us, 4.0 TB/s of the
-// cache, 61% of the copy bandwidth (103 with one f16 for P; 121 for fp32 out).  690 instructions a strip and
-// warp, most of them turning codes into operands, go out at 2.4 a cycle of an SM (of 4): no pipe is full (ALU
-// 48%, tensor 33%, memory 45%), and the four warps a scheduler has, each a chain of dependent steps, wait for
-// fixed latencies (24% of their time) and for the ALU (16%).  Short launches are bound by their dependent steps: 64 blocks of
-// 64 tokens, 8 KV heads: 9.5 us (lookups 1.5, one strip 1.8, the warps' merge 1, partials and their count 1,
-// the last CTA's merge 2).
+// cache, 61% of the copy bandwidth (103 with one f16 for P; 121 for fp32 out).  690 instructions a
+// strip and warp, most of them turning codes into operands, go out at 2.4 a cycle of an SM (of 4): no
+// pipe is full (ALU 48%, tensor 33%, memory 45%), and the four warps a scheduler has, each a chain of
+// dependent steps, wait for fixed latencies (24% of their time) and for the ALU (16%).  Short launches
+// are bound by their dependent steps: 64 blocks of 64 tokens, 8 KV heads: 9.5 us (lookups 1.5, one
+// strip 1.8, the warps' merge 1, partials and their count 1, the last CTA's merge 2).
 #include <float.h>
 #include <math.h>
 

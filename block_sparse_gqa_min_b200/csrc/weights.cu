@@ -296,14 +296,14 @@ __global__ void __launch_bounds__(kThreads, 2) accumulate_weights_kernel(Args a)
 }
 
 // ---------------------------------------------------------------------------
-// Many query rows: the products on tcgen05.  A tile of 128 tokens is the MMA's M, 64 query rows its N:
-// a warp brings its strip of 32 tokens from codes to f16 and stores it as the A operand in tensor
-// memory, one thread issues the eight steps of 16 channels against the rows in shared memory, and every
-// thread reads back the 64 logits of ONE token, so the sum over the rows is in its own registers (no
-// shuffle, no shared memory).  What bounds it is the 16 exponentials a cycle of an SM: 64 rows over 393K tokens
-// and 8 KV heads would take 45 us at that rate and take 104 (four bits; 179 in bf16, where the keys alone
-// take 123; 69 in four bits at 4 rows, where the bytes would take 38): the unit is 47% busy, since a tile's steps (codes to f16 0.4 us, products 0.3, exponentials 0.9)
-// follow one another and tensor memory has room for four tiles an SM.
+// Many query rows: the products on tcgen05.  A tile of 128 tokens is the MMA's M, 64 query rows its N: a warp
+// brings its strip of 32 tokens from codes to f16 and stores it as the A operand in tensor memory, one thread
+// issues the eight steps of 16 channels against the rows in shared memory, and every thread reads back the 64
+// logits of ONE token, so the sum over the rows is in its own registers (no shuffle, no shared memory).  What
+// bounds it is the 16 exponentials a cycle of an SM: 64 rows over 393K tokens and 8 KV heads would take 45 us
+// at that rate and take 104 (four bits; 179 in bf16, where the keys alone take 123; 69 in four bits at 4 rows,
+// where the bytes would take 38): the unit is 47% busy, since a tile's steps (codes to f16 0.4 us, products
+// 0.3, exponentials 0.9) follow one another and tensor memory has room for four tiles an SM.
 // Two CTAs of two warpgroups share an SM; every warpgroup works on tiles of its own, so one's conversion
 // and its wait for the tensor core overlap the others' exponentials.
 // ---------------------------------------------------------------------------

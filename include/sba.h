@@ -524,7 +524,8 @@ int sba_accumulate_weights_kv4(const sba_cache4 *c, const void *q, int32_t M, co
  *            descriptors of the blocks written; gate keys are not refreshed (call
  *            sba_update_descriptors for them).  Rows of dst past the kept ones are left as they were.
  * acc_dst    device fp32 [dst->num_pages][H_kv][b] or NULL: the kept tokens' weights.  Where src and dst share
- *            their rows' pool, acc itself is a good value; otherwise it does not overlap acc.  Cells past the
+ *            their rows' pool, acc itself is a good value (or, where dst's rows begin at a later page of
+ *            it, acc from that page on); otherwise it does not overlap acc.  Cells past the
  *            kept tokens are left as they were: the caller sets a token's cells to 0 when it appends the
  *            token (pages that are used again hold their last tokens' weights).
  * new_lens   device int32 [B]: min(len_s, n_keep); does not overlap src->seq_lens.

@@ -15,7 +15,7 @@ def test_one_pool_shares_its_arrays():
     if torch.cuda.is_available():
         return                                                # (addresses are made up)
     lib, e = sba.load(), ctypes.byref(sba.evict_params(64))
-    acc, new, kept = 0x5000, 0x600000, 0x700000
+    acc, new, kept = 0x50000, 0x600000, 0x700000
 
     def four(src, dst, acc_dst):
         return lib.sba_evict_kv4(c4(**src), acc, e, c4(**dst), acc_dst, new, kept, None)
@@ -36,5 +36,15 @@ def test_one_pool_shares_its_arrays():
     assert four({}, pool, acc + size) == CUDA and four({}, pool, acc + size - 16) == ARG
     assert four(a, b, acc + 16) == ARG
     assert bf16(a, {**b, "v": 0x20000000}, acc) == ARG
+    # a destination that begins at a later page of the pool: its weights at that page, or apart
+    page4, page16, cells = 2 * 2 * 4608, 2 * 64 * 256, 2 * 64 * 4
+    part = dict(block_table=0x900000, desc=None)
+    for pages in (1, 40, -3):
+        later = dict(**part, kv=0x1000 + pages * page4)
+        assert four(a, later, acc + pages * cells) == CUDA and four(a, later, acc + (pages + 1) * cells) == ARG
+        assert four(a, later, acc) == ARG and four(a, later, acc + 2 * size) == CUDA
+        both = dict(**part, k=0x1000 + pages * page16, v=0x2000 + pages * page16)
+        assert bf16(a, both, acc + pages * cells) == CUDA and bf16(a, {**both, "v": 0x2000}, acc + pages * cells) == ARG
+    assert four(a, dict(**part, kv=0x1000 + 16), acc) == ARG
     # descriptors of another pool are another array, unless its own table keeps the pages apart
     assert four({}, dict(kv=0x10000000), None) == ARG and four(a, dict(kv=0x10000000), None) == ARG
